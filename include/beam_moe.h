@@ -329,6 +329,145 @@ int beam_moe_forward_noalloc(const beam_moe_config* cfg, int64_t T, const void* 
                              const void* w13_scale, const void* w2, const void* w2_scale,
                              void* y, int32_t* ids_out, float* weights_out, void* stream);
 
+/*
+ * Training operators: what a fine-tuning step, or a caller that runs the experts' products
+ * itself (other weights, adapters, experts on other devices), needs around the products.
+ *   forward    beam_moe_route -> sort -> dispatch -> gate/up product -> swiglu -> down
+ *              product -> combine
+ *   backward   combine_backward -> down product's gradients -> swiglu_backward -> gate/up
+ *              product's gradients -> dispatch_backward -> route_backward
+ * They read fewer fields of cfg than the layer (each entry point says which); act_dtype is
+ * F32 or BF16 (else BEAM_ERR_UNSUPPORTED), 1 <= topk <= 32, n_experts in [1, 256], any
+ * hidden and inter >= 1.  T * topk <= INT32_MAX / 2, and no array holds 2^40 elements or
+ * more (BEAM_ERR_INVALID_ARG).  No kernel reads or writes outside the arrays whose sizes
+ * the call states, whatever the index arrays hold.
+ *
+ * Pairs and rows.  Pair p = t * K + i is pick i of token t.  row_of_pair[p] is the row that
+ * holds it in a buffer of `rows` rows; a value outside [0, rows) means that the pair is
+ * dropped (a padding token, an expert of another device, a row past a capacity): it is
+ * neither read nor written, adds nothing to a sum and gets a zero gradient.  Live pairs
+ * must have distinct rows.  Rows that belong to no pair are left as they were.
+ *
+ * The 8-bit copy of a row (to keep for the backward pass, 1.03 bytes a value): E4M3 codes
+ * and, per block of 32 columns from column 0 (the last block may be shorter), one E8M0
+ * exponent byte c: value = code * 2^(c - 127).  c is the least for which the block's
+ * largest magnitude is at most 448 * 2^(c - 127), at least 0 (so 0 for a block of zeros);
+ * a code is the one rounding (to nearest even) of value * 2^(127 - c).  A block with an
+ * infinity or a NaN has c = 255 and reads back as NaN.
+ */
+
+/*
+ * Sort: rows for the pairs, by expert and, within an expert, in pair order.
+ *   cfg         n_experts (E) and topk (K) are read
+ *   ids         device [T, K] int32 expert ids; an id outside [0, E) drops its pair.  A
+ *               caller with experts [lo, hi) passes id - lo and E = hi - lo
+ *   expert_off  device [E+1] int32 out: first row of each expert, and the number of rows
+ *   row_of_pair device [T, K] int32 out: row of each pair, -1 if dropped
+ *   pair_of_row device [T*K] int32 out: pair of each row, -1 from row expert_off[E] on
+ *   ws          device workspace of ws_bytes >= beam_moe_sort_workspace_size(cfg, T),
+ *               which is 0 (NULL is accepted) up to 8192 pairs
+ * T == 0 writes expert_off (zeros).
+ */
+size_t beam_moe_sort_workspace_size(const beam_moe_config* cfg, int64_t T);
+
+int beam_moe_sort(const beam_moe_config* cfg, int64_t T, const int32_t* ids, int32_t* expert_off,
+                  int32_t* row_of_pair, int32_t* pair_of_row, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dispatch: xs[row_of_pair[t, i]] = x[t].
+ *   cfg         hidden (H), topk and act_dtype are read
+ *   x           device [T, H] act_dtype; with x_scale, its 8-bit copy: [T, H] E4M3 codes
+ *   x_scale     device [T, ceil(H/32)] E8M0 bytes, or NULL
+ *   row_of_pair device [T, K] int32; NULL (topk must be 1): row t for token t
+ *   xs          device [rows, H] act_dtype out, or NULL with keep_q (the copy alone)
+ *   keep_q, keep_scale  device [T, H] and [T, ceil(H/32)] bytes out: the 8-bit copy of all
+ *               of x; both or neither, and not together with x_scale
+ */
+int beam_moe_dispatch(const beam_moe_config* cfg, int64_t T, const void* x, const uint8_t* x_scale,
+                      const int32_t* row_of_pair, int64_t rows, void* xs, uint8_t* keep_q, uint8_t* keep_scale,
+                      void* stream);
+
+/*
+ * Gradient of dispatch: dx[t] = sum_i dxs[row_of_pair[t, i]], i ascending, FP32 sums.
+ *   cfg         hidden, topk and act_dtype are read
+ *   dxs         device [rows, H] act_dtype;  dx  device [T, H] act_dtype out
+ */
+int beam_moe_dispatch_backward(const beam_moe_config* cfg, int64_t T, const void* dxs, const int32_t* row_of_pair,
+                               int64_t rows, void* dx, void* stream);
+
+/*
+ * Combine: y[t] = sum_i weights[t, i] * expert_out[row_of_pair[t, i]], i ascending, FP32
+ * sums.  cfg, row_of_pair, rows: as above; weights device [T, K] FP32.
+ */
+int beam_moe_combine(const beam_moe_config* cfg, int64_t T, const void* expert_out, const int32_t* row_of_pair,
+                     int64_t rows, const float* weights, void* y, void* stream);
+
+/*
+ * Gradient of combine, p = (t, i) with row r:
+ *   dexpert_out[r] = weights[p] * dy[t],   dweights[p] = <dy[t], expert_out[r]>  (FP32)
+ *   expert_out, dweights  both or neither (NULL: the weights' gradient is not wanted, as
+ *               when the weights were applied in beam_moe_swiglu)
+ *   dexpert_out device [rows, H] act_dtype out; may be expert_out itself
+ */
+int beam_moe_combine_backward(const beam_moe_config* cfg, int64_t T, const void* dy, const void* expert_out,
+                              const int32_t* row_of_pair, int64_t rows, const float* weights, void* dexpert_out,
+                              float* dweights, void* stream);
+
+/*
+ * SwiGLU between the experts' products, h[r] = weights[p] * SiLU(g) * u with (g, u) the
+ * halves of gu[r], FP32 inside.  The weights may be applied here instead of in combine
+ * (combine then takes ones): the backward pass needs no expert outputs then.
+ *   cfg         inter (I), topk and act_dtype are read
+ *   gu          device [rows, 2I] act_dtype (gate columns, then up columns)
+ *   row_of_pair device [T, K] int32; NULL (topk must be 1): row t for token t (dense MLP)
+ *   weights     device [T, K] FP32, or NULL (ones)
+ *   h           device [rows, I] act_dtype out
+ *   keep_q      device [rows, 2I] bytes out, keep_scale device [rows, 2, ceil(I/32)] bytes
+ *               out: the 8-bit copy of gu, each half blocked on its own; both or neither
+ */
+int beam_moe_swiglu(const beam_moe_config* cfg, int64_t T, const void* gu, const int32_t* row_of_pair, int64_t rows,
+                    const float* weights, void* h, uint8_t* keep_q, uint8_t* keep_scale, void* stream);
+
+/*
+ * Gradient of swiglu, s = sigma(g):
+ *   dg = w dh u s (1 + g (1 - s)),  du = w dh g s,  dweights[p] = sum over the row of dh g s u
+ *   gu          device [rows, 2I] act_dtype; with gu_scale, its 8-bit copy (E4M3 codes)
+ *   gu_scale    device [rows, 2, ceil(I/32)] E8M0 bytes, or NULL
+ *   dgu         device [rows, 2I] act_dtype out; may be gu itself without gu_scale
+ *   h           device [rows, I] act_dtype out, or NULL: beam_moe_swiglu's result again from
+ *               these g and u (the down weights' gradient needs it); may be dh itself
+ *   dweights    device [T, K] FP32 out, or NULL; needs weights
+ */
+int beam_moe_swiglu_backward(const beam_moe_config* cfg, int64_t T, const void* dh, const void* gu,
+                             const uint8_t* gu_scale, const int32_t* row_of_pair, int64_t rows, const float* weights,
+                             void* dgu, void* h, float* dweights, void* stream);
+
+/*
+ * Gradient of the router: with s_i = sigma(logit of pick i), p_i = s_i / sum_j s_j and
+ * weights w_i = alpha p_i (beam_moe_route), from the weights' gradients g_i
+ *   dz_i = alpha p_i (1 - s_i) sum_j p_j (g_i - g_j)           (FP32)
+ *   dx[t] = dx_add[t] + sum_i dz_i w_router[:, e_i],  dw_router[:, e] = sum_t x[t] dz[t, e],
+ *   dlogit_bias[e] = sum_t dz[t, e].
+ * The choice of experts (and select_bias) has no gradient.
+ *   cfg         hidden (at most 2^20), n_experts, topk, routed_scale and act_dtype are read
+ *   x           device [T, H] act_dtype, what the router read (FP32 xhat in the sublayer)
+ *   w_router    device [H, E] FP32
+ *   logits      device [T, E] FP32: the `logits` region of beam_moe_route's workspace
+ *   ids         device [T, K] int32; an id outside [0, E) is no pick: it enters no sum (for
+ *               padding tokens; to leave out single picks, pass zero gradients for them)
+ *   dweights    device [T, K] FP32
+ *   dx_add      device [T, H] act_dtype (the gradient from the experts), or NULL
+ *   dx          device [T, H] act_dtype out, or NULL (then dx_add too); may be dx_add itself
+ *   dw_router   device [H, E] FP32 out;  dlogit_bias device [E] FP32 out, or NULL
+ *   ws          device workspace, ws_bytes >= beam_moe_route_backward_workspace_size(cfg, T)
+ * T == 0 writes zeros into dw_router and dlogit_bias.
+ */
+size_t beam_moe_route_backward_workspace_size(const beam_moe_config* cfg, int64_t T);
+
+int beam_moe_route_backward(const beam_moe_config* cfg, int64_t T, const void* x, const float* w_router,
+                            const float* logits, const int32_t* ids, const float* dweights, const void* dx_add,
+                            void* dx, float* dw_router, float* dlogit_bias, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

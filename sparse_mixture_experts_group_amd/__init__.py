@@ -21,7 +21,10 @@ BEAM_FP8_SCALES_FP32, BEAM_FP8_SCALES_POW2 = range(2)
 C_FUNCTIONS = ("beam_moe_status_string", "beam_moe_abi_version", "beam_moe_workspace_size",
                "beam_moe_workspace_map", "beam_moe_route", "beam_moe_forward",
                "beam_moe_sublayer_forward", "beam_moe_time_kernel", "beam_dense_workspace_size",
-               "beam_dense_forward", "beam_dense_sublayer_forward", "beam_moe_forward_noalloc")
+               "beam_dense_forward", "beam_dense_sublayer_forward", "beam_moe_forward_noalloc",
+               "beam_moe_sort_workspace_size", "beam_moe_sort", "beam_moe_dispatch", "beam_moe_dispatch_backward",
+               "beam_moe_combine", "beam_moe_combine_backward", "beam_moe_swiglu", "beam_moe_swiglu_backward",
+               "beam_moe_route_backward_workspace_size", "beam_moe_route_backward")
 BEAM_KERNEL_NONE, BEAM_KERNEL_ROUTER_LOGITS, BEAM_KERNEL_GATE_UP, BEAM_KERNEL_DOWN, BEAM_KERNEL_COMBINE = range(5)
 
 
@@ -102,6 +105,26 @@ def lib() -> ctypes.CDLL:
     L.beam_dense_sublayer_forward.restype = ctypes.c_int
     L.beam_dense_sublayer_forward.argtypes = [cfgp, i64, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz,
                                               vp]
+    L.beam_moe_sort_workspace_size.restype = sz
+    L.beam_moe_sort_workspace_size.argtypes = [cfgp, i64]
+    L.beam_moe_sort.restype = ctypes.c_int
+    L.beam_moe_sort.argtypes = [cfgp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.beam_moe_dispatch.restype = ctypes.c_int
+    L.beam_moe_dispatch.argtypes = [cfgp, i64, vp, vp, vp, i64, vp, vp, vp, vp]
+    L.beam_moe_dispatch_backward.restype = ctypes.c_int
+    L.beam_moe_dispatch_backward.argtypes = [cfgp, i64, vp, vp, i64, vp, vp]
+    L.beam_moe_combine.restype = ctypes.c_int
+    L.beam_moe_combine.argtypes = [cfgp, i64, vp, vp, i64, vp, vp, vp]
+    L.beam_moe_combine_backward.restype = ctypes.c_int
+    L.beam_moe_combine_backward.argtypes = [cfgp, i64, vp, vp, vp, i64, vp, vp, vp, vp]
+    L.beam_moe_swiglu.restype = ctypes.c_int
+    L.beam_moe_swiglu.argtypes = [cfgp, i64, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.beam_moe_swiglu_backward.restype = ctypes.c_int
+    L.beam_moe_swiglu_backward.argtypes = [cfgp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.beam_moe_route_backward_workspace_size.restype = sz
+    L.beam_moe_route_backward_workspace_size.argtypes = [cfgp, i64]
+    L.beam_moe_route_backward.restype = ctypes.c_int
+    L.beam_moe_route_backward.argtypes = [cfgp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -296,3 +319,277 @@ def beam_dense_sublayer_forward(cfg, h, step_k, w13, w2, pre_gain=None, post_gai
                                            _stream(stream))
     _check(st, "beam_dense_sublayer_forward")
     return h
+
+
+# ---------------------------------------------------------------------------
+# training operators
+# ---------------------------------------------------------------------------
+KEEP_BLOCK = 32          # columns that share one exponent of the 8-bit copy
+
+
+def keep_blocks(cols: int) -> int:
+    """Exponent bytes of one row of `cols` columns."""
+    return -(-cols // KEEP_BLOCK)
+
+
+def _act_torch(cfg):
+    import torch
+    t = {BEAM_DTYPE_F32: torch.float32, BEAM_DTYPE_BF16: torch.bfloat16}.get(cfg.act_dtype)
+    if t is None:
+        raise BeamMoEError(BEAM_ERR_UNSUPPORTED, "act_dtype")
+    return t
+
+
+def _arg(name, t, shape, *dtypes):
+    """Checks one tensor's dtype and shape and that it is dense; returns its address (None
+    for None; an empty tensor has none)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)}, "
+                         f"got {t.dtype} of shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr() or None
+
+
+class _On:
+    """Where a training operator runs: the device of its tensors (all on one GPU), and the
+    caller's stream or that device's current one.  Inside the context the device is
+    current and tensors are allocated for that stream, so a temporary of this call is not
+    handed out again before the stream is done with it."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("tensor must be on the GPU")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        self.device = dev
+        current = torch.cuda.current_stream(dev)
+        self.stream = current if stream is None else stream
+        self.handle = self.stream.cuda_stream
+        here = dev.index == torch.cuda.current_device()
+        self._enter = None if here and self.stream == current else torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self._enter is not None:
+            self._enter.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._enter is not None:
+            self._enter.__exit__(*exc)
+        return False
+
+
+def _rows_by(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def route_logits(cfg, T, ws):
+    """The logits [T, E] that the last beam_moe_route or forward call left in its workspace
+    (a view; beam_moe_route_backward reads them)."""
+    import torch
+    at = beam_moe_workspace_map(cfg, T)["logits"]
+    return ws[at:at + 4 * T * cfg.n_experts].view(torch.float32).view(T, cfg.n_experts)
+
+
+def beam_moe_sort_workspace_size(cfg: beam_moe_config, T: int) -> int:
+    return int(lib().beam_moe_sort_workspace_size(ctypes.byref(cfg), int(T)))
+
+
+def beam_moe_sort(cfg, ids, expert_off=None, row_of_pair=None, pair_of_row=None, ws=None, stream=None):
+    """Rows for the picks `ids` [T, K] int32, by expert: (expert_off [E+1], row_of_pair
+    [T, K], pair_of_row [T*K]), all int32.  Ids outside [0, E) are dropped (row -1)."""
+    import torch
+    i32 = torch.int32
+    T, K, E = _rows_by(ids, "ids"), cfg.topk, cfg.n_experts
+    with _On(stream, ids, expert_off, row_of_pair, pair_of_row, ws) as on:
+        p_ids = _arg("ids", ids, (T, K), i32)
+        expert_off = torch.empty(max(E + 1, 1), dtype=i32, device=on.device) if expert_off is None else expert_off
+        row_of_pair = torch.empty((T, K), dtype=i32, device=on.device) if row_of_pair is None else row_of_pair
+        pair_of_row = torch.empty(T * K, dtype=i32, device=on.device) if pair_of_row is None else pair_of_row
+        if ws is None:
+            need = beam_moe_sort_workspace_size(cfg, T)
+            ws = torch.empty(need, dtype=torch.uint8, device=on.device) if need else None
+        st = lib().beam_moe_sort(ctypes.byref(cfg), T, p_ids, _arg("expert_off", expert_off, (E + 1,), i32),
+                                 _arg("row_of_pair", row_of_pair, (T, K), i32),
+                                 _arg("pair_of_row", pair_of_row, (T * K,), i32),
+                                 None if ws is None else _ptr(ws),
+                                 0 if ws is None else ws.numel() * ws.element_size(), on.handle)
+    _check(st, "beam_moe_sort")
+    return expert_off, row_of_pair, pair_of_row
+
+
+def beam_moe_dispatch(cfg, x, row_of_pair, xs=None, rows=None, x_scale=None, keep8=False, keep_q=None,
+                      keep_scale=None, stream=None):
+    """xs[row_of_pair[t, i]] = x[t]: returns xs [rows, H] (rows: T*K by default; those of no
+    pair are left as they were).  x_scale: x holds the codes of an 8-bit copy.  keep8 (or
+    keep_q and keep_scale): returns (xs, keep_q, keep_scale) with the 8-bit copy of x;
+    rows=0 makes the copy alone (xs is None).  row_of_pair None: row t for token t."""
+    import torch
+    T, K, H, act = _rows_by(x, "x"), cfg.topk, cfg.hidden, _act_torch(cfg)
+    u8, f8 = torch.uint8, torch.float8_e4m3fn
+    with _On(stream, x, row_of_pair, xs, x_scale, keep_q, keep_scale) as on:
+        if xs is not None:
+            rows = _rows_by(xs, "xs")
+        rows = T * K if rows is None else int(rows)
+        p_x = _arg("x", x, (T, H), *((act,) if x_scale is None else (f8, u8)))
+        if xs is None and rows > 0:
+            xs = torch.empty((rows, H), dtype=act, device=on.device)
+        if keep8 and keep_q is None:
+            keep_q = torch.empty((T, H), dtype=f8, device=on.device)
+        if keep8 and keep_scale is None:
+            keep_scale = torch.empty((T, keep_blocks(H)), dtype=u8, device=on.device)
+        st = lib().beam_moe_dispatch(ctypes.byref(cfg), T, p_x, _arg("x_scale", x_scale, (T, keep_blocks(H)), u8),
+                                     _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
+                                     _arg("xs", xs, (rows, H), act), _arg("keep_q", keep_q, (T, H), f8, u8),
+                                     _arg("keep_scale", keep_scale, (T, keep_blocks(H)), u8), on.handle)
+    _check(st, "beam_moe_dispatch")
+    return xs if keep_q is None else (xs, keep_q, keep_scale)
+
+
+def beam_moe_dispatch_backward(cfg, dxs, row_of_pair, dx=None, stream=None):
+    """dx[t] = sum of the gradients dxs [rows, H] of token t's rows: returns dx [T, H]."""
+    import torch
+    rows, T, K, H, act = _rows_by(dxs, "dxs"), _rows_by(row_of_pair, "row_of_pair"), cfg.topk, cfg.hidden, _act_torch(cfg)
+    with _On(stream, dxs, row_of_pair, dx) as on:
+        dx = torch.empty((T, H), dtype=act, device=on.device) if dx is None else dx
+        st = lib().beam_moe_dispatch_backward(ctypes.byref(cfg), T, _arg("dxs", dxs, (rows, H), act),
+                                              _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
+                                              _arg("dx", dx, (T, H), act), on.handle)
+    _check(st, "beam_moe_dispatch_backward")
+    return dx
+
+
+def beam_moe_combine(cfg, expert_out, row_of_pair, weights, y=None, stream=None):
+    """y[t] = sum_i weights[t, i] * expert_out[row_of_pair[t, i]]: returns y [T, H]."""
+    import torch
+    rows, T, K, H, act = (_rows_by(expert_out, "expert_out"), _rows_by(row_of_pair, "row_of_pair"), cfg.topk, cfg.hidden,
+                          _act_torch(cfg))
+    with _On(stream, expert_out, row_of_pair, weights, y) as on:
+        y = torch.empty((T, H), dtype=act, device=on.device) if y is None else y
+        st = lib().beam_moe_combine(ctypes.byref(cfg), T, _arg("expert_out", expert_out, (rows, H), act),
+                                    _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
+                                    _arg("weights", weights, (T, K), torch.float32), _arg("y", y, (T, H), act),
+                                    on.handle)
+    _check(st, "beam_moe_combine")
+    return y
+
+
+def beam_moe_combine_backward(cfg, dy, expert_out, row_of_pair, weights, deo=None, dweights=None, rows=None,
+                              stream=None):
+    """Gradients of combine: (deo [rows, H], dweights [T, K]).  expert_out None: (deo, None),
+    with `rows` rows (T*K by default).  deo may be expert_out itself."""
+    import torch
+    T, K, H, act = _rows_by(dy, "dy"), cfg.topk, cfg.hidden, _act_torch(cfg)
+    with _On(stream, dy, expert_out, row_of_pair, weights, deo, dweights) as on:
+        for t in (deo, expert_out):
+            rows = _rows_by(t, "rows") if t is not None else rows
+        rows = T * K if rows is None else int(rows)
+        deo = torch.empty((rows, H), dtype=act, device=on.device) if deo is None else deo
+        if expert_out is not None and dweights is None:
+            dweights = torch.empty((T, K), dtype=torch.float32, device=on.device)
+        p_eo = _arg("expert_out", expert_out, (rows, H), act)
+        p_dw = _arg("dweights", dweights, (T, K), torch.float32)
+        if expert_out is not None and rows == 0:       # no row to read: every pair is dropped
+            dweights.zero_()
+            p_eo = p_dw = None
+        st = lib().beam_moe_combine_backward(ctypes.byref(cfg), T, _arg("dy", dy, (T, H), act), p_eo,
+                                             _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
+                                             _arg("weights", weights, (T, K), torch.float32),
+                                             _arg("deo", deo, (rows, H), act), p_dw, on.handle)
+    _check(st, "beam_moe_combine_backward")
+    return deo, dweights
+
+
+def beam_moe_swiglu(cfg, gu, weights=None, row_of_pair=None, h=None, keep8=False, keep_q=None, keep_scale=None,
+                    stream=None):
+    """h[r] = weights[p] * SiLU(g) * u for the rows r of the pairs p, (g, u) the halves of gu
+    [rows, 2I]: returns h [rows, I], with keep8 (or keep_q and keep_scale) (h, keep_q,
+    keep_scale) with the 8-bit copy of gu.  row_of_pair None: row t for token t (K = 1)."""
+    import torch
+    rows, K, I, act = _rows_by(gu, "gu"), cfg.topk, cfg.inter, _act_torch(cfg)
+    T = rows if row_of_pair is None else _rows_by(row_of_pair, "row_of_pair")
+    u8, f8 = torch.uint8, torch.float8_e4m3fn
+    with _On(stream, gu, weights, row_of_pair, h, keep_q, keep_scale) as on:
+        h = torch.empty((rows, I), dtype=act, device=on.device) if h is None else h
+        if keep8 and keep_q is None:
+            keep_q = torch.empty((rows, 2 * I), dtype=f8, device=on.device)
+        if keep8 and keep_scale is None:
+            keep_scale = torch.empty((rows, 2, keep_blocks(I)), dtype=u8, device=on.device)
+        st = lib().beam_moe_swiglu(ctypes.byref(cfg), T, _arg("gu", gu, (rows, 2 * I), act),
+                                   _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
+                                   _arg("weights", weights, (T, K), torch.float32), _arg("h", h, (rows, I), act),
+                                   _arg("keep_q", keep_q, (rows, 2 * I), f8, u8),
+                                   _arg("keep_scale", keep_scale, (rows, 2, keep_blocks(I)), u8), on.handle)
+    _check(st, "beam_moe_swiglu")
+    return h if keep_q is None else (h, keep_q, keep_scale)
+
+
+def beam_moe_swiglu_backward(cfg, dh, gu, gu_scale=None, weights=None, row_of_pair=None, dgu=None, h=None,
+                             dweights=None, again=True, stream=None):
+    """Gradients of swiglu from gu, or from its 8-bit copy with gu_scale: (dgu [rows, 2I],
+    h [rows, I] computed again, or None with again=False, dweights [T, K], or None without
+    weights).  dgu may be gu itself (not a copy), h may be dh itself."""
+    import torch
+    rows, K, I, act = _rows_by(gu, "gu"), cfg.topk, cfg.inter, _act_torch(cfg)
+    T = rows if row_of_pair is None else _rows_by(row_of_pair, "row_of_pair")
+    u8, f8, f32 = torch.uint8, torch.float8_e4m3fn, torch.float32
+    with _On(stream, dh, gu, gu_scale, weights, row_of_pair, dgu, h, dweights) as on:
+        dgu = torch.empty((rows, 2 * I), dtype=act, device=on.device) if dgu is None else dgu
+        if again and h is None:
+            h = torch.empty((rows, I), dtype=act, device=on.device)
+        if weights is not None and dweights is None:
+            dweights = torch.empty((T, K), dtype=f32, device=on.device)
+        st = lib().beam_moe_swiglu_backward(ctypes.byref(cfg), T, _arg("dh", dh, (rows, I), act),
+                                            _arg("gu", gu, (rows, 2 * I), *((act,) if gu_scale is None else (f8, u8))),
+                                            _arg("gu_scale", gu_scale, (rows, 2, keep_blocks(I)), u8),
+                                            _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
+                                            _arg("weights", weights, (T, K), f32),
+                                            _arg("dgu", dgu, (rows, 2 * I), act), _arg("h", h, (rows, I), act),
+                                            _arg("dweights", dweights, (T, K), f32), on.handle)
+    _check(st, "beam_moe_swiglu_backward")
+    return dgu, h, dweights
+
+
+def beam_moe_route_backward_workspace_size(cfg: beam_moe_config, T: int) -> int:
+    return int(lib().beam_moe_route_backward_workspace_size(ctypes.byref(cfg), int(T)))
+
+
+def beam_moe_route_backward(cfg, x, w_router, logits, ids, dweights, dx_add=None, dx=None, dw_router=None,
+                            dlogit_bias=None, ws=None, stream=None):
+    """Gradients of the router's weights: (dx [T, H] = dx_add + the router's part, dw_router
+    [H, E], dlogit_bias [E]).  logits [T, E]: `route_logits` of the forward call's
+    workspace.  dx may be dx_add itself."""
+    import torch
+    T, K, H, E, act = _rows_by(x, "x"), cfg.topk, cfg.hidden, cfg.n_experts, _act_torch(cfg)
+    i32, f32 = torch.int32, torch.float32
+    with _On(stream, x, w_router, logits, ids, dweights, dx_add, dx, dw_router, dlogit_bias, ws) as on:
+        dx = torch.empty((T, H), dtype=act, device=on.device) if dx is None else dx
+        dw_router = torch.empty((H, E), dtype=f32, device=on.device) if dw_router is None else dw_router
+        dlogit_bias = torch.empty(E, dtype=f32, device=on.device) if dlogit_bias is None else dlogit_bias
+        if ws is None:
+            need = beam_moe_route_backward_workspace_size(cfg, T)
+            ws = torch.empty(need, dtype=torch.uint8, device=on.device) if need else None
+        st = lib().beam_moe_route_backward(ctypes.byref(cfg), T, _arg("x", x, (T, H), act),
+                                           _arg("w_router", w_router, (H, E), f32), _arg("logits", logits, (T, E), f32),
+                                           _arg("ids", ids, (T, K), i32), _arg("dweights", dweights, (T, K), f32),
+                                           _arg("dx_add", dx_add, (T, H), act), _arg("dx", dx, (T, H), act),
+                                           _arg("dw_router", dw_router, (H, E), f32),
+                                           _arg("dlogit_bias", dlogit_bias, (E,), f32),
+                                           None if ws is None else _ptr(ws),
+                                           0 if ws is None else ws.numel() * ws.element_size(), on.handle)
+    _check(st, "beam_moe_route_backward")
+    return dx, dw_router, dlogit_bias

@@ -1,0 +1,72 @@
+// Launchers of the training operators (dispatch, combine, SwiGLU with an 8-bit copy,
+// router gradient).  Arguments have been checked by train_api.hip.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace beam {
+
+// ---- sort (dispatch.hip) --------------------------------------------------
+// Pairs that one block ranks: a batch of at most this many is sorted by one launch of one
+// block, a larger one by blocks of kSortChunk (count, scan over the blocks, scatter).
+constexpr int kSortSingle = 8192;
+constexpr int kSortChunk = 2048;
+inline int64_t sort_blocks(int64_t pairs) { return pairs <= kSortSingle ? 0 : (pairs + kSortChunk - 1) / kSortChunk; }
+
+// counts: [sort_blocks * E] int32 and totals: [E] int32 of workspace (unused for one block).
+void launch_sort_pairs(hipStream_t st, int64_t pairs, int E, const int32_t* ids, int32_t* expert_off,
+                       int32_t* row_of_pair, int32_t* pair_of_row, int32_t* counts, int32_t* totals);
+
+// ---- rows (dispatch.hip) --------------------------------------------------
+struct RowArgs {
+    int64_t T;                   // tokens
+    int64_t rows;                // rows of the sorted buffers
+    int H, K;
+    bool bf16;
+    const int32_t* row_of_pair;  // [T, K], or null: K = 1 and row = token
+    const float* weights;        // [T, K] or null (ones)
+};
+
+// xs[row] = x[t] (x_scale: x holds E4M3 codes); keep_q / keep_scale: the 8-bit copy of x.
+void launch_dispatch(hipStream_t st, const RowArgs& a, const void* x, const uint8_t* x_scale, void* xs,
+                     uint8_t* keep_q, uint8_t* keep_scale);
+// y[t] = sum_i w_i in[row_i]
+void launch_combine_rows(hipStream_t st, const RowArgs& a, const void* in, void* y);
+// deo[row_i] = w_i dy[t], dweights[t, i] = <dy[t], eo[row_i]> (eo null: deo only)
+void launch_combine_backward(hipStream_t st, const RowArgs& a, const void* dy, const void* eo, void* deo,
+                             float* dweights);
+
+// ---- SwiGLU (swiglu_train.hip) ---------------------------------------------
+struct SwigluArgs {
+    int64_t pairs;               // pairs (rows of the dense MLP)
+    int64_t rows;                // rows of the buffers
+    int I;
+    bool bf16;
+    const int32_t* row_of_pair;  // [pairs] or null: row = pair
+    const float* weights;        // [pairs] or null (ones)
+};
+
+void launch_swiglu(hipStream_t st, const SwigluArgs& a, const void* gu, void* h, uint8_t* keep_q, uint8_t* keep_scale);
+// gu_scale: gu holds E4M3 codes.  h and dweights may be null.
+void launch_swiglu_backward(hipStream_t st, const SwigluArgs& a, const void* dh, const void* gu,
+                            const uint8_t* gu_scale, void* dgu, void* h, float* dweights);
+
+// ---- router gradient (route_backward.hip) ----------------------------------
+struct RouteBackwardArgs {
+    int64_t T;
+    int H, E, K;
+    float alpha;
+    bool bf16;                   // x, dx_add, dx
+};
+
+struct RouteBackwardPlan {
+    int splits;                  // token ranges whose partial dW_r are added up
+    size_t dz, expert, part, total;   // workspace offsets and size
+};
+RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K);
+void launch_route_backward(hipStream_t st, const RouteBackwardArgs& a, const RouteBackwardPlan& plan, const void* x,
+                           const float* w_router, const float* logits, const int32_t* ids, const float* dweights,
+                           const void* dx_add, void* dx, float* dw_router, float* dlogit_bias, void* ws);
+
+}  // namespace beam
