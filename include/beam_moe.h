@@ -353,7 +353,9 @@ int beam_moe_forward_noalloc(const beam_moe_config* cfg, int64_t T, const void* 
  * exponent byte c: value = code * 2^(c - 127).  c is the least for which the block's
  * largest magnitude is at most 448 * 2^(c - 127), at least 0 (so 0 for a block of zeros);
  * a code is the one rounding (to nearest even) of value * 2^(127 - c).  A block with an
- * infinity or a NaN has c = 255 and reads back as NaN.
+ * infinity or a NaN has c = 255 and reads back as NaN.  Reading back rounds only where
+ * value leaves the type's range: a finite value of at least 248 * 2^120 (3.3e38) is kept as
+ * 256 * 2^120 and reads back as infinity.
  */
 
 /*

@@ -441,12 +441,13 @@ def beam_moe_dispatch(cfg, x, row_of_pair, xs=None, rows=None, x_scale=None, kee
     import torch
     T, K, H, act = _rows_by(x, "x"), cfg.topk, cfg.hidden, _act_torch(cfg)
     u8, f8 = torch.uint8, torch.float8_e4m3fn
+    copy_alone = xs is None and rows == 0
     with _On(stream, x, row_of_pair, xs, x_scale, keep_q, keep_scale) as on:
         if xs is not None:
             rows = _rows_by(xs, "xs")
         rows = T * K if rows is None else int(rows)
         p_x = _arg("x", x, (T, H), *((act,) if x_scale is None else (f8, u8)))
-        if xs is None and rows > 0:
+        if xs is None and not copy_alone:
             xs = torch.empty((rows, H), dtype=act, device=on.device)
         if keep8 and keep_q is None:
             keep_q = torch.empty((T, H), dtype=f8, device=on.device)

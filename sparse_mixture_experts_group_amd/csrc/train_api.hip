@@ -91,9 +91,9 @@ int beam_moe_dispatch(const beam_moe_config* cfg, int64_t T, const void* x, cons
                       void* stream) {
     int s = check_rows_call(cfg, T, rows);
     if (s != BEAM_OK) return s;
+    if (T == 0) return BEAM_OK;
     if (!row_of_pair && cfg->topk != 1) return BEAM_ERR_INVALID_ARG;
     if ((keep_q != nullptr) != (keep_scale != nullptr) || (keep_q && x_scale)) return BEAM_ERR_INVALID_ARG;
-    if (T == 0) return BEAM_OK;
     if (!given(x) || !optional(x_scale) || !optional(row_of_pair)) return BEAM_ERR_INVALID_ARG;
     if (!optional(xs) || !optional(keep_q) || !optional(keep_scale)) return BEAM_ERR_INVALID_ARG;
     if (rows == 0) xs = nullptr;              // no row can be written
@@ -148,7 +148,7 @@ static int check_swiglu(const beam_moe_config* cfg, int64_t T, const int32_t* ro
     if (s != BEAM_OK) return s;
     if (rows < 0 || rows > INT32_MAX || cfg->inter > INT32_MAX / 2 || rows > kMaxElements / cfg->inter)
         return BEAM_ERR_INVALID_ARG;
-    if (!row_of_pair && cfg->topk != 1) return BEAM_ERR_INVALID_ARG;
+    if (T > 0 && !row_of_pair && cfg->topk != 1) return BEAM_ERR_INVALID_ARG;
     return check_act(cfg);
 }
 

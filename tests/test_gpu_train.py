@@ -1,0 +1,730 @@
+"""Training operators on the GPU against plain FP64 formulas on the CPU.
+
+Tolerances.  u = 2^-24 is half a step of FP32, eps_out half a step of the stored type
+(BF16 2^-8, FP32 2^-24, relative to the value).  A sum of n products in FP32 is off by at
+most (n + 1) u times the sum of the products' magnitudes (n the longest chain of
+additions; the bounds below count a row's full width, more than any chain has).  The
+SwiGLU's sigma is within (|g| + 8) 2^-23 of the true one, relatively: the exponential's
+argument g log2 e is off by |g| u, its exponential and the reciprocal by a step each, the
+sum 1 + e by half of one.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_group_amd as bm
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+EPS = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
+ACT = {"f32": bm.BEAM_DTYPE_F32, "bf16": bm.BEAM_DTYPE_BF16}
+
+
+def config(dt, H=1, I=1, E=2, K=1, alpha=2.5):
+    return bm.make_config(hidden=H, inter=I, n_experts=E, topk=K, act_dtype=ACT[dt], routed_scale=alpha)
+
+
+def rand(seed, *shape, dt="f32", scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(TORCH[dt])
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy() if t.dtype != torch.float8_e4m3fn else t.detach().cpu().float().double().numpy()
+
+
+def within(got, want, bound, what=""):
+    got, want = f64(got), np.asarray(want)
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.max(np.abs(got - want)[bad]):.3g}"
+
+
+def picks(seed, T, E, K, drop=0.0, skew=False):
+    """[T, K] int32 ids: distinct experts where E allows; a share of picks and one token in
+    five dropped by ids outside [0, E)."""
+    r = np.random.default_rng(seed)
+    if skew:
+        ids = np.minimum((r.random((T, K)) ** 3 * E).astype(np.int32), E - 1)    # repeats too
+    elif K <= E:
+        ids = np.argsort(r.random((T, E)), 1)[:, :K].astype(np.int32)
+    else:
+        ids = r.integers(0, E, (T, K), dtype=np.int32)
+    if drop:
+        ids = np.where(r.random((T, K)) < drop, r.choice([-1, -7, E, E + 300, 2 ** 30, -2 ** 31], (T, K)), ids)
+        ids[r.random(T) < 0.2] = -1
+    return torch.from_numpy(ids.astype(np.int32))
+
+
+def sorted_rows(ids, E):
+    """(expert_off, row_of_pair, pair_of_row) by a stable sort."""
+    flat = ids.numpy().reshape(-1)
+    live = np.flatnonzero((flat >= 0) & (flat < E))
+    order = live[np.argsort(flat[live], kind="stable")]
+    row = np.full(flat.size, -1, np.int32)
+    row[order] = np.arange(order.size)
+    pair = np.full(flat.size, -1, np.int32)
+    pair[:order.size] = order
+    off = np.concatenate([[0], np.cumsum(np.bincount(flat[live], minlength=E))]).astype(np.int32)
+    return off, row.reshape(ids.shape), pair
+
+
+def keep_ref(x):
+    """8-bit copy of the last axis in FP64: (values of the codes, exponent bytes)."""
+    x = np.asarray(x, np.float64)
+    C = x.shape[-1]
+    nb = -(-C // 32)
+    v = np.zeros(x.shape[:-1] + (nb * 32,))
+    v[..., :C] = x
+    v = v.reshape(x.shape[:-1] + (nb, 32))
+    big = np.abs(v).max(-1)
+    grid = 2.0 ** np.arange(-127, 128)
+    n = np.searchsorted(448 * grid, big) - 127                    # least n with amax <= 448 2^n
+    y = v / 2.0 ** n[..., None]
+    e = np.maximum(np.frexp(y)[1] - 1, -6)
+    codes = np.round(y / 2.0 ** (e - 3)) * 2.0 ** (e - 3)
+    return codes.reshape(x.shape[:-1] + (nb * 32,))[..., :C], (n + 127).astype(np.uint8)
+
+
+def restore(codes, scale, C):
+    return codes * np.repeat(2.0 ** (scale.astype(np.float64) - 127), 32, -1)[..., :C]
+
+
+# ---------------------------------------------------------------------------
+# sort
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,E,K,drop,skew", [
+    (1, 1, 1, 0, False), (1, 256, 8, 0, False), (3, 2, 1, 0.5, False), (64, 256, 8, 0, False), (65, 60, 8, 0.3, False),
+    (512, 3, 1, 0, False), (513, 256, 1, 0.1, True), (1024, 256, 8, 0, True), (1025, 255, 8, 0.2, False),
+    (2731, 2, 3, 0, True), (4099, 256, 8, 0.1, True), (700, 256, 32, 0.05, False), (20001, 17, 5, 0.4, True),
+    (66000, 256, 8, 0, False)])
+def test_sort(T, E, K, drop, skew):
+    ids = picks(T, T, E, K, drop, skew)
+    off, row, pair = bm.beam_moe_sort(config("f32", E=E, K=K), ids.cuda())
+    r_off, r_row, r_pair = sorted_rows(ids, E)
+    assert np.array_equal(off.cpu().numpy(), r_off)
+    assert np.array_equal(row.cpu().numpy(), r_row)
+    assert np.array_equal(pair.cpu().numpy(), r_pair)
+
+
+@pytest.mark.parametrize("T", [0, 5, 3000])
+def test_sort_of_nothing(T):
+    ids = torch.full((T, 4), -1, dtype=torch.int32)
+    out = torch.full((10,), 77, dtype=torch.int32, device="cuda")
+    off, row, pair = bm.beam_moe_sort(config("f32", E=9, K=4), ids.cuda(), expert_off=out)
+    assert off is out and (off == 0).all() and (row == -1).all() and (pair == -1).all()
+
+
+# ---------------------------------------------------------------------------
+# dispatch and combine
+# ---------------------------------------------------------------------------
+SHAPES = [  # T, H, E, K, drop
+    (1, 1, 1, 1, 0), (1, 5120, 256, 8, 0), (5, 7, 3, 2, 0.3), (17, 32, 256, 8, 0.3), (33, 33, 60, 9, 0.2),
+    (9, 64, 4, 4, 0), (40, 257, 16, 6, 0.3), (130, 520, 32, 32, 0.1), (64, 1001, 7, 3, 0), (300, 1000, 256, 8, 0.2),
+    (2100, 96, 12, 2, 0.3), (3, 12000, 8, 5, 0.3), (2049, 640, 9, 1, 0)]
+
+
+def routed(seed, T, E, K, drop):
+    ids = picks(seed, T, E, K, drop)
+    _, row, pair = sorted_rows(ids, E)
+    return row, pair, torch.from_numpy(row).cuda()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E,K,drop", SHAPES)
+def test_dispatch(T, H, E, K, drop, dt):
+    row, pair, row_d = routed(H, T, E, K, drop)
+    cfg = config(dt, H=H, E=E, K=K)
+    x = rand(1, T, H, dt=dt)
+    if drop:
+        x[(row < 0).all(1)] = float("nan")                 # tokens without rows are not copied
+    want = np.full((T * K, H), -3.0)
+    want[pair >= 0] = f64(x)[pair[pair >= 0] // K]
+    xs = torch.full((T * K, H), -3.0, dtype=TORCH[dt], device="cuda")
+    assert bm.beam_moe_dispatch(cfg, x.cuda(), row_d, xs=xs) is xs
+    within(xs, want, 0.0, "xs")
+    # fewer rows than pairs: those past the buffer are dropped
+    cap = max(1, T * K // 2)
+    guard = torch.full((cap + 1, H), -3.0, dtype=TORCH[dt], device="cuda")
+    bm.beam_moe_dispatch(cfg, x.cuda(), row_d, xs=guard[:cap])
+    within(guard[:cap], want[:cap], 0.0, "capacity")
+    assert (guard[cap:] == -3.0).all()
+    # with the 8-bit copy, the copy alone, and out of the copy
+    xc = torch.nan_to_num(x, nan=0.5)
+    codes, scale = keep_ref(f64(xc))
+    xs.fill_(-3.0)
+    got, q, s = bm.beam_moe_dispatch(cfg, xc.cuda(), row_d, xs=xs, keep8=True)
+    within(got, want, 0.0, "xs beside the copy")
+    within(q, codes, 0.0, "codes")
+    assert np.array_equal(s.cpu().numpy(), scale)
+    none, q2, s2 = bm.beam_moe_dispatch(cfg, xc.cuda(), row_d, rows=0, keep8=True)
+    assert none is None and torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
+    xs.fill_(-3.0)
+    bm.beam_moe_dispatch(cfg, q, row_d, xs=xs, x_scale=s)
+    want[pair >= 0] = restore(codes, scale, H)[pair[pair >= 0] // K]
+    within(xs, want, 0.0, "restored")                      # four bits fit both types
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E,K,drop", SHAPES)
+def test_combine_and_gradients(T, H, E, K, drop, dt):
+    row, pair, row_d = routed(T + H, T, E, K, drop)
+    cfg = config(dt, H=H, E=E, K=K)
+    live = row >= 0
+    at = np.where(live, row, 0)
+    eo = rand(2, T * K, H, dt=dt)
+    eo[pair < 0] = float("nan")                            # rows of no pair are not read
+    w = rand(3, T, K).abs()
+    w[~torch.from_numpy(live)] = float("nan")
+    w64, eo64 = np.where(live, f64(w), 0), np.nan_to_num(f64(eo))
+    prod = w64[..., None] * (eo64[at] * live[..., None])
+    y = bm.beam_moe_combine(cfg, eo.cuda(), row_d, w.cuda())
+    mag = np.abs(prod).sum(1)
+    within(y, prod.sum(1), (K + 1) * U * mag + EPS[dt] * (np.abs(prod.sum(1)) + K * U * mag), "y")
+    # gradient of dispatch
+    one = eo64[at] * live[..., None]
+    mag = np.abs(one).sum(1)
+    dx = bm.beam_moe_dispatch_backward(cfg, eo.cuda(), row_d)
+    within(dx, one.sum(1), K * U * mag + EPS[dt] * (np.abs(one.sum(1)) + K * U * mag), "dx")
+    # gradient of combine
+    dy = rand(4, T, H, dt=dt)
+    deo = torch.full((T * K, H), -3.0, dtype=TORCH[dt], device="cuda")
+    got, dw = bm.beam_moe_combine_backward(cfg, dy.cuda(), eo.cuda(), row_d, w.cuda(), deo=deo)
+    dy64 = f64(dy)
+    want = np.full((T * K, H), -3.0)
+    back = pair >= 0
+    want[back] = w64.reshape(-1)[pair[back], None] * dy64[pair[back] // K]
+    within(got, want, (U + EPS[dt]) * (1 + U) * np.abs(want) * back[:, None], "deo")
+    terms = dy64[:, None, :] * one
+    within(dw, terms.sum(-1), (H + 1) * U * np.abs(terms).sum(-1), "dweights")
+    # without the weights' gradient, and in place
+    alone, none = bm.beam_moe_combine_backward(cfg, dy.cuda(), None, row_d, w.cuda(), deo=torch.full_like(deo, -3.0))
+    assert none is None and torch.equal(alone, deo)
+    here = torch.where(torch.from_numpy(back)[:, None], eo, torch.full_like(eo, -3.0)).cuda()
+    same, dw2 = bm.beam_moe_combine_backward(cfg, dy.cuda(), here, row_d, w.cuda(), deo=here)
+    assert same is here and torch.equal(here, deo) and torch.equal(dw2, dw)
+
+
+def test_no_tokens_and_no_rows():
+    for dt in ("bf16", "f32"):
+        cfg = config(dt, H=24, I=24, E=4, K=2)
+        none = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+        e = torch.empty((0, 24), dtype=TORCH[dt], device="cuda")
+        assert bm.beam_moe_dispatch(cfg, e, none).shape == (0, 24)
+        assert bm.beam_moe_combine(cfg, e, none, none.float()).shape == (0, 24)
+        assert bm.beam_moe_dispatch_backward(cfg, e, none).shape == (0, 24)
+        deo, dw = bm.beam_moe_combine_backward(cfg, e, e, none, none.float())
+        assert deo.shape == (0, 24) and dw.shape == (0, 2)
+        # tokens, all of them dropped, and a buffer without rows
+        row = torch.full((5, 2), -1, dtype=torch.int32, device="cuda")
+        w = torch.full((5, 2), float("nan"), device="cuda")
+        assert (bm.beam_moe_combine(cfg, e, row, w) == 0).all()
+        assert (bm.beam_moe_dispatch_backward(cfg, e, row) == 0).all()
+        dy = torch.ones((5, 24), dtype=TORCH[dt], device="cuda")
+        deo, dw = bm.beam_moe_combine_backward(cfg, dy, e, row, w)
+        assert deo.shape == (0, 24) and (dw == 0).all()
+        gu = torch.empty((0, 48), dtype=TORCH[dt], device="cuda")
+        assert bm.beam_moe_swiglu(cfg, gu, weights=w, row_of_pair=row).shape == (0, 24)
+        dgu, h, dw = bm.beam_moe_swiglu_backward(cfg, e, gu, weights=w, row_of_pair=row)
+        assert dgu.shape == (0, 48) and (dw == 0).all()
+
+
+def test_index_values_outside_the_buffer_are_dropped():
+    """Rows that no sort gives (other values, far out of range) count as dropped."""
+    cfg = config("bf16", H=40, E=4, K=3)
+    row = torch.tensor([[0, 6, -5], [2 ** 31 - 1, 3, -2 ** 31], [5, 1, 2]], dtype=torch.int32)
+    live = (row >= 0) & (row < 6)
+    x, eo, w = rand(1, 3, 40, dt="bf16"), rand(2, 6, 40, dt="bf16"), rand(3, 3, 3)
+    xs = bm.beam_moe_dispatch(cfg, x.cuda(), row.cuda(), xs=torch.zeros((6, 40), dtype=torch.bfloat16, device="cuda"))
+    want = torch.zeros(6, 40, dtype=torch.bfloat16)
+    for t in range(3):
+        for i in range(3):
+            if live[t, i]:
+                want[row[t, i]] = x[t]
+    assert torch.equal(xs.cpu(), want)
+    y = bm.beam_moe_combine(cfg, eo.cuda(), row.cuda(), w.cuda())
+    prod = f64(w)[..., None] * f64(eo)[np.where(live, row, 0)] * live.numpy()[..., None]
+    within(y, prod.sum(1), EPS["bf16"] * np.abs(prod.sum(1)) + 5 * U * np.abs(prod).sum(1))
+    deo, dw = bm.beam_moe_combine_backward(cfg, x.cuda(), eo.cuda(), row.cuda(), w.cuda())
+    assert (dw.cpu()[~live] == 0).all() and (dw.cpu()[live] != 0).all()
+
+
+def test_offsets_past_32_bits():
+    """Rows whose element offsets pass 2^31 and byte offsets 2^32."""
+    T, K, H = 33000, 8, 8192
+    cfg = config("bf16", H=H, E=8, K=K)
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    ids = torch.arange(8, dtype=torch.int32, device="cuda").repeat(T, 1)
+    _, row, pair = bm.beam_moe_sort(cfg, ids)
+    xs = bm.beam_moe_dispatch(cfg, x, row)
+    assert xs.numel() > 2 ** 31
+    for lo in (0, T * K - 5000):                            # expert 7's rows are the last T
+        assert torch.equal(xs[lo:lo + 5000], x[(pair[lo:lo + 5000] // K).long()])
+    w = torch.full((T, K), 0.125, device="cuda")
+    assert torch.equal(bm.beam_moe_combine(cfg, xs, row, w), x)        # eight equal halves of a power of two
+    deo, dw = bm.beam_moe_combine_backward(cfg, x, xs, row, w, deo=xs)
+    assert torch.equal(deo[-5000:], (x[-5000:].float() * 0.125).to(torch.bfloat16))
+    sq = x[-1].double().square().sum()
+    assert ((dw[-1].double() - sq).abs() <= (H + 1) * U * sq).all()
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit copy at its borders
+# ---------------------------------------------------------------------------
+def test_keep_borders():
+    """Exponents at the edges of a binade, blocks of zeros, the smallest and largest values,
+    ties, infinities and NaN."""
+    cfg = config("f32", H=32, E=2, K=1)
+    big = np.float32(448.0)
+    rows = [np.zeros(32)]
+    for v in (big, np.nextafter(big, np.float32(np.inf)), big * 2.0 ** -20, np.nextafter(big, np.float32(0)),
+              np.finfo(np.float32).max, 2.0 ** -149, 2.0 ** -126, 448 * 2.0 ** -127, 449 * 2.0 ** -127, 1.0, 1.75, 1.76):
+        rows.append(np.full(32, v) * np.linspace(-1, 1, 32))
+    rows.append(np.concatenate([[448.0], (np.arange(31) + 0.5) * 2]))          # ties between codes
+    x = torch.from_numpy(np.stack(rows).astype(np.float32))
+    codes, scale = keep_ref(f64(x))
+    none, q, s = bm.beam_moe_dispatch(cfg, x.cuda(), None, rows=0, keep8=True)
+    within(q, codes, 0.0, "codes")
+    assert np.array_equal(s.cpu().numpy(), scale)
+    back = bm.beam_moe_dispatch(cfg, q, None, x_scale=s)
+    # code * 2^n, rounded once to FP32: subnormal results, and 256 * 2^120 past its range
+    with np.errstate(over="ignore"):
+        want = restore(codes, scale, 32).astype(np.float32)
+    assert np.array_equal(back.cpu().numpy(), want) and np.isinf(want).sum() == 2
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        y = torch.ones(2, 64)
+        y[1, 40] = bad
+        c2 = config("f32", H=64, E=2, K=1)
+        _, q, s = bm.beam_moe_dispatch(c2, y.cuda(), None, rows=0, keep8=True)
+        back = bm.beam_moe_dispatch(c2, q, None, x_scale=s).cpu()
+        assert s[1, 1] == 255 and (s.cpu() != 255).sum() == 3
+        assert torch.isnan(back[1, 32:]).all() and torch.equal(back[0], y[0]) and torch.equal(back[1, :32], y[1, :32])
+
+
+# ---------------------------------------------------------------------------
+# SwiGLU
+# ---------------------------------------------------------------------------
+SWIGLU = [  # T, I, E, K, drop
+    (1, 1, 1, 1, 0), (16, 2560, 256, 8, 0), (5, 7, 3, 2, 0.3), (17, 32, 16, 8, 0.3), (33, 33, 60, 9, 0.2),
+    (40, 257, 16, 6, 0.3), (64, 1001, 7, 3, 0), (300, 504, 256, 8, 0.2), (700, 96, 12, 3, 0.3), (3, 20480, 8, 2, 0.3)]
+
+
+def swiglu_ref(gu, w, I):
+    g, u = gu[:, :I], gu[:, I:]
+    s = 1 / (1 + np.exp(-np.clip(g, -700, 700)))
+    return g, u, s, w[:, None] * g * s * u
+
+
+def swiglu_check(dt, I, K, row, pair, gu_t, w, dh_t, source8):
+    """Forward (from gu) or backward (from gu or its copy) against the formulas."""
+    cfg = config(dt, I=I, E=4, K=K)
+    R = gu_t.shape[0]
+    back = np.ones(R, bool) if pair is None else pair >= 0
+    row_d = None if row is None else torch.from_numpy(row).cuda()
+    w_d = None if w is None else w.cuda()
+    wr = np.ones(R)
+    if w is not None:
+        wr[back] = f64(w).reshape(-1)[pair[back]]
+        wr[~back] = 0
+    gu = np.nan_to_num(f64(gu_t))
+    rel = lambda g: (np.abs(g) + 8) * 2.0 ** -23 + 6 * U
+    hbuf = torch.full((R, I), -3.0, dtype=TORCH[dt], device="cuda")
+    qbuf = torch.full((R, 2 * I), 9, dtype=torch.uint8, device="cuda")
+    sbuf = torch.full((R, 2, bm.keep_blocks(I)), 9, dtype=torch.uint8, device="cuda")
+    h, q, scale = bm.beam_moe_swiglu(cfg, gu_t.cuda(), weights=w_d, row_of_pair=row_d, h=hbuf, keep_q=qbuf,
+                                     keep_scale=sbuf)
+    g, u, s, h64 = swiglu_ref(gu, wr, I)
+    # the hardware reciprocal gives no subnormal: a sigma below 2^-126 is 0, so a product
+    # with it is off by its other factors times 2^-126
+    cut = 2.0 ** -126
+    tiny = cut * np.abs(wr[:, None] * g * u)
+    want = np.where(back[:, None], h64, -3.0)
+    within(h, want, ((rel(g) + EPS[dt]) * np.abs(h64) * 1.01 + tiny) * back[:, None], "h")
+    codes, exps = keep_ref(gu.reshape(R, 2, I))
+    codes = codes.reshape(R, 2 * I)
+    got = q.view(torch.float8_e4m3fn)
+    nine = float(torch.tensor(9, dtype=torch.uint8).view(torch.float8_e4m3fn).float())
+    within(got, np.where(back[:, None], codes, nine), 0.0, "codes")
+    assert np.array_equal(scale.cpu().numpy(), np.where(back[:, None, None], exps, 9))
+    plain = bm.beam_moe_swiglu(cfg, gu_t.cuda(), weights=w_d, row_of_pair=row_d, h=torch.full_like(hbuf, -3.0))
+    assert torch.equal(plain, h)
+    # backward
+    src, src_scale = gu_t.cuda(), None
+    if source8:
+        gu = restore(codes.reshape(R, 2, I), exps, I).reshape(R, 2 * I)
+        src, src_scale = q, scale
+        g, u, s, h64 = swiglu_ref(gu, wr, I)
+    dgu_b = torch.full((R, 2 * I), -3.0, dtype=TORCH[dt], device="cuda")
+    hb = torch.full((R, I), -3.0, dtype=TORCH[dt], device="cuda")
+    dgu, h2, dw = bm.beam_moe_swiglu_backward(cfg, dh_t.cuda(), src, gu_scale=src_scale, weights=w_d, row_of_pair=row_d,
+                                              dgu=dgu_b, h=hb)
+    dh = np.nan_to_num(f64(dh_t))
+    tiny = cut * np.abs(wr[:, None] * g * u)
+    a = np.abs(wr[:, None] * dh * u)
+    dg64 = wr[:, None] * dh * u * s * (1 + g * (1 - s))
+    du64 = wr[:, None] * dh * g * s
+    bg = a * s * (1 + np.abs(g)) * (2 * rel(g) + 4 * U) + EPS[dt] * np.abs(dg64) * 1.01
+    bu = (rel(g) + EPS[dt]) * np.abs(du64) * 1.01
+    live = back[:, None]
+    within(dgu[:, :I], np.where(live, dg64, -3.0), (bg + cut * a * (1 + np.abs(g))) * live, "dg")
+    within(dgu[:, I:], np.where(live, du64, -3.0), (bu + cut * np.abs(wr[:, None] * dh * g)) * live, "du")
+    within(h2, np.where(live, h64, -3.0), ((rel(g) + EPS[dt]) * np.abs(h64) * 1.01 + tiny) * live, "h again")
+    if w is None:
+        assert dw is None
+    else:
+        terms = dh * g * s * u
+        want = np.zeros(w.numel())
+        want[pair[back]] = terms.sum(1)[back]
+        bound = np.zeros(w.numel())
+        bound[pair[back]] = ((rel(g) + (I + 1) * U) * np.abs(terms) + cut * np.abs(dh * g * u)).sum(1)[back]
+        within(dw.reshape(-1), want, bound, "dweights")
+    # no second h; in place over gu and dh
+    dgu3, none, _ = bm.beam_moe_swiglu_backward(cfg, dh_t.cuda(), src, gu_scale=src_scale, weights=w_d, row_of_pair=row_d,
+                                                dgu=torch.full_like(dgu, -3.0), again=False)
+    assert none is None and torch.equal(dgu3, dgu)
+    if not source8:
+        over, dover = gu_t.cuda(), dh_t.cuda()
+        bm.beam_moe_swiglu_backward(cfg, dover, over, weights=w_d, row_of_pair=row_d, dgu=over, h=dover)
+        keep = torch.from_numpy(back).cuda()
+        assert torch.equal(over[keep], dgu[keep]) and torch.equal(dover[keep], h2[keep])
+
+
+@pytest.mark.parametrize("source8", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,I,E,K,drop", SWIGLU)
+def test_swiglu(T, I, E, K, drop, dt, source8):
+    row, pair, _ = routed(T + I, T, E, K, drop)
+    gu, dh, w = rand(1, T * K, 2 * I, dt=dt, scale=3.0), rand(2, T * K, I, dt=dt), rand(3, T, K).abs()
+    gu[pair < 0] = float("nan")
+    dh[pair < 0] = float("nan")
+    w[torch.from_numpy(row < 0)] = float("nan")
+    swiglu_check(dt, I, K, row, pair, gu, w, dh, source8)
+
+
+@pytest.mark.parametrize("source8", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,I", [(1, 20480), (70, 260), (2500, 72)])
+def test_swiglu_dense(T, I, dt, source8):
+    swiglu_check(dt, I, 1, None, None, rand(1, T, 2 * I, dt=dt, scale=3.0), None, rand(2, T, I, dt=dt), source8)
+
+
+def test_swiglu_far_arguments():
+    """Gates far out: sigma saturates without NaN, gradients go to their limits."""
+    g = torch.tensor([0.0, -0.0, 1e-30, 30.0, 88.0, 200.0, 1e30, -30.0, -87.0, -88.5, -104.0, -200.0, -1e30, 1.2785, -1.2785,
+                      5.0]).repeat(2, 1)
+    u = torch.linspace(-2, 2, 16).repeat(2, 1)
+    swiglu_check("f32", 16, 1, None, None, torch.cat([g, u], 1), None, torch.ones(2, 16), False)
+
+
+# ---------------------------------------------------------------------------
+# router gradient
+# ---------------------------------------------------------------------------
+def route_ref(x, wr, z, ids, gw, add, alpha):
+    """(dx, dW, db, and bounds' magnitudes) in FP64."""
+    T, K = ids.shape
+    E = wr.shape[1]
+    live = (ids >= 0) & (ids < E)
+    at = np.where(live, ids, 0)
+    zz = np.clip(np.take_along_axis(z, at, 1), -87, 87)
+    s = live / (1 + np.exp(-zz))
+    d = s.sum(1, keepdims=True)
+    p = np.divide(s, d, out=np.zeros_like(s), where=d > 0)
+    g = np.where(live, gw, 0)
+    f = alpha * p / (1 + np.exp(zz))
+    diff = g[:, :, None] - g[:, None, :]
+    dz = f * (p[:, None, :] * diff).sum(-1)
+    dzm = np.abs(f) * (p[:, None, :] * np.abs(diff)).sum(-1)
+    dense, densem = np.zeros((T, E)), np.zeros((T, E))
+    for i in range(K):
+        np.add.at(dense, (np.arange(T), at[:, i]), dz[:, i])
+        np.add.at(densem, (np.arange(T), at[:, i]), dzm[:, i])
+    return (add + dense @ wr.T, x.T @ dense, dense.sum(0), densem @ np.abs(wr).T, np.abs(x).T @ densem, densem.sum(0))
+
+
+ROUTE = [  # T, H, E, K, drop
+    (1, 1, 1, 1, 0), (1, 130, 256, 8, 0), (16, 5120, 256, 8, 0), (7, 127, 3, 2, 0.3), (33, 128, 60, 9, 0.2),
+    (65, 129, 16, 6, 0.3), (200, 300, 255, 8, 0.2), (130, 64, 256, 32, 0.1), (1500, 257, 12, 3, 0.3),
+    (900, 1024, 256, 8, 0), (64, 33000, 5, 2, 0)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E,K,drop", ROUTE)
+def test_route_backward(T, H, E, K, drop, dt):
+    ids = picks(H + T, T, E, K, drop)
+    cfg = config(dt, H=H, E=E, K=K, alpha=1.75)
+    z, gw = rand(1, T, E, scale=3.0), rand(2, T, K)
+    x, add, wr = rand(3, T, H, dt=dt), rand(4, T, H, dt=dt), rand(5, H, E)
+    gone = ((ids < 0) | (ids >= E)).all(1)
+    x[gone] = float("nan")                                 # padding tokens are not read
+    gw[(ids < 0) | (ids >= E)] = float("nan")
+    ref = route_ref(np.nan_to_num(f64(x)), f64(wr), f64(z), ids.numpy(), np.nan_to_num(f64(gw)), f64(add), 1.75)
+    dx, dwr, db = bm.beam_moe_route_backward(cfg, x.cuda(), wr.cuda(), z.cuda(), ids.cuda(), gw.cuda(), dx_add=add.cuda())
+    # dz: sigma and 1 - sigma within 6 steps each (exponential 3, sum, division), the sums
+    # over K picks, four products
+    rdz = (K + 24) * 2.0 ** -23
+    within(dx, ref[0], (rdz + (K + 1) * U) * ref[3] + K * U * np.abs(ref[0]) + EPS[dt] * np.abs(ref[0]) * 1.01, "dx")
+    within(dwr, ref[1], (rdz + (T + 8) * U) * ref[4], "dw_router")
+    within(db, ref[2], (rdz + (T + 8) * U) * ref[5], "dlogit_bias")
+    # nothing added; in place; without dx at the C entry's own width
+    alone, dwr2, db2 = bm.beam_moe_route_backward(cfg, x.cuda(), wr.cuda(), z.cuda(), ids.cuda(), gw.cuda())
+    within(alone, ref[0] - f64(add), (rdz + (K + 1) * U) * ref[3] + EPS[dt] * np.abs(ref[0] - f64(add)) * 1.01, "dx alone")
+    assert torch.equal(dwr2, dwr) and torch.equal(db2, db)
+    here = add.cuda()
+    bm.beam_moe_route_backward(cfg, x.cuda(), wr.cuda(), z.cuda(), ids.cuda(), gw.cuda(), dx_add=here, dx=here)
+    assert torch.equal(here, dx)
+
+
+def test_route_backward_same_expert_twice_and_no_tokens():
+    T, H, E, K = 50, 40, 6, 4
+    cfg = config("f32", H=H, E=E, K=K, alpha=1.75)
+    ids = picks(1, T, E, K, 0, skew=True)
+    assert any(len(set(r)) < K for r in ids.tolist())
+    z, gw, x, wr = rand(1, T, E), rand(2, T, K), rand(3, T, H), rand(5, H, E)
+    ref = route_ref(f64(x), f64(wr), f64(z), ids.numpy(), f64(gw), np.zeros((T, H)), 1.75)
+    dx, dwr, db = bm.beam_moe_route_backward(cfg, x.cuda(), wr.cuda(), z.cuda(), ids.cuda(), gw.cuda())
+    rdz = (K + 24) * 2.0 ** -23
+    within(dx, ref[0], (rdz + (K + 2) * U) * ref[3] + U * np.abs(ref[0]), "dx")
+    within(dwr, ref[1], (rdz + (T * K + 8) * U) * ref[4], "dw_router")
+    within(db, ref[2], (rdz + (T * K + 8) * U) * ref[5], "dlogit_bias")
+    e = torch.empty((0, H), device="cuda")
+    out = torch.full((H, E), 5.0, device="cuda")
+    dx, dwr, db = bm.beam_moe_route_backward(cfg, e, wr.cuda(), torch.empty((0, E), device="cuda"),
+                                             torch.empty((0, K), dtype=torch.int32, device="cuda"),
+                                             torch.empty((0, K), device="cuda"), dw_router=out)
+    assert dx.shape == (0, H) and (out == 0).all() and (db == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# together: a training step of the layer
+# ---------------------------------------------------------------------------
+LAYER = dict(T=70, H=128, I=64, E=16, K=4)
+
+
+def expert_products(a, w, off):
+    """Rows of each expert times its matrix (the caller's own products)."""
+    out = torch.zeros((a.shape[0], w.shape[1]), dtype=a.dtype, device=a.device)
+    for e in range(w.shape[0]):
+        out[off[e]:off[e + 1]] = a[off[e]:off[e + 1]] @ w[e].t()
+    return out
+
+
+def train_step(cfg, x, wr, w13, w2, dy, in_swiglu, keep8, ids=None):
+    """Forward and backward of the layer with the operators around plain products; the
+    weights are applied in swiglu or in combine.  Returns y, ids and all gradients."""
+    T, K, E, I = x.shape[0], cfg.topk, cfg.n_experts, cfg.inter
+    ws = bm.alloc_workspace(cfg, T)
+    ids, w = bm.beam_moe_route(cfg, x, wr, ws=ws)
+    logits = bm.route_logits(cfg, T, ws)
+    off_d, row, pair = bm.beam_moe_sort(cfg, ids)
+    off = off_d.tolist()
+    sw, ones = (w, torch.ones_like(w)) if in_swiglu else (None, None)
+    if keep8:
+        xs, xq, xscale = bm.beam_moe_dispatch(cfg, x, row, keep8=True)
+    else:
+        xs = bm.beam_moe_dispatch(cfg, x, row)
+    gu = expert_products(xs, w13, off)
+    got = bm.beam_moe_swiglu(cfg, gu, weights=sw, row_of_pair=row, keep8=keep8)
+    h = got[0] if keep8 else got
+    eo = expert_products(h, w2, off)
+    y = bm.beam_moe_combine(cfg, eo, row, ones if in_swiglu else w)
+    # backward
+    deo, dw = bm.beam_moe_combine_backward(cfg, dy, None if in_swiglu else eo, row, ones if in_swiglu else w)
+    dh = expert_products(deo, w2.transpose(1, 2).contiguous(), off)
+    src, scale = (got[1], got[2]) if keep8 else (gu, None)
+    dgu, h, dws = bm.beam_moe_swiglu_backward(cfg, dh, src, gu_scale=scale, weights=sw, row_of_pair=row)
+    dw = dws if in_swiglu else dw
+    if keep8:
+        xs = bm.beam_moe_dispatch(cfg, xq, row, x_scale=xscale)
+    dw2, dw13 = torch.zeros_like(w2), torch.zeros_like(w13)
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        dw2[e], dw13[e] = deo[r].t() @ h[r], dgu[r].t() @ xs[r]
+    dxs = expert_products(dgu, w13.transpose(1, 2).contiguous(), off)
+    dx = bm.beam_moe_dispatch_backward(cfg, dxs, row)
+    dx, dwr, db = bm.beam_moe_route_backward(cfg, x, wr, logits, ids, dw, dx_add=dx, dx=dx)
+    return dict(y=y, ids=ids, dx=dx, dw13=dw13, dw2=dw2, dwr=dwr, db=db)
+
+
+def layer_loss(x, wr, bias, w13, w2, dy, ids, alpha):
+    """<layer(x), dy> in FP64 with the choice of experts fixed."""
+    I = w2.shape[2]
+    s = torch.sigmoid(x @ wr + bias).gather(1, ids)
+    w = alpha * s / s.sum(1, keepdim=True)
+    gu = torch.einsum("th,tkoh->tko", x, w13[ids])
+    h = torch.nn.functional.silu(gu[..., :I]) * gu[..., I:]
+    y = (torch.einsum("tki,tkhi->tkh", h, w2[ids]) * w[..., None]).sum(1)
+    return (y * dy).sum(), y
+
+
+@pytest.mark.parametrize("in_swiglu", [False, True])
+def test_training_step_gradients(in_swiglu):
+    """FP32: against autograd of the FP64 layer, against differences of it, and the forward
+    pass against the fused layer.  The FP32 products and sums (of at most 128 terms a
+    product, 70 tokens a weight) leave relative errors near 1e-6 of an array's norm; the
+    bound is 2e-5."""
+    T, H, I, E, K = (LAYER[k] for k in "THIEK")
+    cfg = bm.make_config(hidden=H, inter=I, n_experts=E, n_groups=4, topk_groups=2, topk=K, act_dtype=0, weight_dtype=0)
+    x, wr, dy = rand(1, T, H), rand(2, H, E, scale=H ** -0.5), rand(3, T, H)
+    w13, w2 = rand(4, E, 2 * I, H, scale=H ** -0.5), rand(5, E, H, I, scale=I ** -0.5)
+    got = train_step(cfg, *(t.cuda() for t in (x, wr, w13, w2, dy)), in_swiglu, False)
+    fused = bm.beam_moe_forward(cfg, x.cuda(), wr.cuda(), w13.cuda(), w2.cuda())
+    assert (fused - got["y"]).norm() <= 2e-5 * fused.norm()
+    leaves = {n: t.double().requires_grad_() for n, t in (("dx", x), ("dwr", wr), ("dw13", w13), ("dw2", w2))}
+    leaves["db"] = torch.zeros(E, dtype=torch.float64, requires_grad=True)
+    ids = got["ids"].cpu().long()
+    args = lambda v: (v["dx"], v["dwr"], v["db"], v["dw13"], v["dw2"], dy.double(), ids, 2.5)
+    loss, y = layer_loss(*args(leaves))
+    loss.backward()
+    assert (got["y"].cpu().double() - y).norm() <= 2e-5 * y.norm()
+    for n, leaf in leaves.items():
+        g = got[n].cpu().double()
+        assert (g - leaf.grad).norm() <= 2e-5 * leaf.grad.norm(), n
+        # differences: along a direction d, (L(v + t d) - L(v - t d)) / 2t is <grad, d> up to
+        # t^2 of third derivatives (1e-8 here) and 1e-16 L / t of rounding
+        d = torch.randn(leaf.shape, generator=torch.Generator().manual_seed(9), dtype=torch.float64)
+        t = 1e-4 / d.norm()
+        with torch.no_grad():
+            at = lambda sign: layer_loss(*args({**leaves, n: leaf + sign * t * d}))[0]
+            slope = (at(1) - at(-1)) / (2 * t)
+        assert abs((g * d).sum() - slope) <= 2e-5 * g.norm() * d.norm(), n
+
+
+def test_training_step_in_8_bits():
+    """BF16 with the 8-bit copies: the step runs, its forward pass is that without copies
+    bit for bit, and its gradients are those of the restored values.  A restored value is
+    off by at most 2^-4 of itself (or 2^-10 of its block's largest, for small ones); the
+    gradients are linear or smooth in them, so an array's relative difference stays under
+    2^-4 times a small factor: 0.2 bounds it, 1e-3 at least shows that the copies are used."""
+    T, H, I, E, K = (LAYER[k] for k in "THIEK")
+    cfg = bm.make_config(hidden=256, inter=128, n_experts=E, n_groups=4, topk_groups=2, topk=K)
+    H, I = 256, 128
+    x, wr, dy = rand(1, T, H, dt="bf16"), rand(2, H, E, scale=H ** -0.5), rand(3, T, H, dt="bf16")
+    w13, w2 = rand(4, E, 2 * I, H, dt="bf16", scale=H ** -0.5), rand(5, E, H, I, dt="bf16", scale=I ** -0.5)
+    args = [t.cuda() for t in (x, wr, w13, w2, dy)]
+    full, kept = train_step(cfg, *args, True, False), train_step(cfg, *args, True, True)
+    assert torch.equal(full["y"], kept["y"]) and torch.equal(full["ids"], kept["ids"])
+    for n in ("dx", "dw13", "dw2", "dwr", "db"):
+        a, b = full[n].double(), kept[n].double()
+        assert 1e-3 * a.norm() < (a - b).norm() < 0.2 * a.norm(), n
+
+
+# ---------------------------------------------------------------------------
+# how they are called: graphs, streams, refusals
+# ---------------------------------------------------------------------------
+def step_calls(cfg, b):
+    """The operators in a row on fixed buffers, without host work between them."""
+    off, row, pair = bm.beam_moe_sort(cfg, b["ids"])
+    xs, xq, xscale = bm.beam_moe_dispatch(cfg, b["x"], row, xs=torch.zeros_like(b["eo"]), keep8=True)
+    y = bm.beam_moe_combine(cfg, b["eo"], row, b["w"])
+    deo, dw = bm.beam_moe_combine_backward(cfg, b["dy"], b["eo"], row, b["w"], deo=torch.zeros_like(b["eo"]))
+    h, gq, gscale = bm.beam_moe_swiglu(cfg, b["gu"], weights=b["w"], row_of_pair=row, h=torch.zeros_like(b["dh"]),
+                                       keep_q=torch.zeros(b["gu"].shape, dtype=torch.uint8, device="cuda"),
+                                       keep_scale=torch.zeros((b["gu"].shape[0], 2, bm.keep_blocks(cfg.inter)),
+                                                              dtype=torch.uint8, device="cuda"))
+    dgu, h2, dws = bm.beam_moe_swiglu_backward(cfg, b["dh"], gq, gu_scale=gscale, weights=b["w"], row_of_pair=row,
+                                               dgu=torch.zeros_like(b["gu"]), h=torch.zeros_like(b["dh"]))
+    dx = bm.beam_moe_dispatch_backward(cfg, deo, row)
+    dx, dwr, db = bm.beam_moe_route_backward(cfg, b["x"], b["wr"], b["z"], b["ids"], dw, dx_add=dx)
+    return [off, row, pair, xs, xq.view(torch.uint8), xscale, y, deo, dw, h, gq, gscale, dgu, h2, dws, dx, dwr, db]
+
+
+def step_buffers(seed, T, H, I, E, K):
+    R = T * K
+    b = dict(ids=picks(seed, T, E, K, 0.1), x=rand(seed, T, H, dt="bf16"), eo=rand(seed + 1, R, H, dt="bf16"),
+             w=rand(seed + 2, T, K).abs(), dy=rand(seed + 3, T, H, dt="bf16"), gu=rand(seed + 4, R, 2 * I, dt="bf16"),
+             dh=rand(seed + 5, R, I, dt="bf16"), wr=rand(seed + 6, H, E), z=rand(seed + 7, T, E))
+    return {k: v.cuda() for k, v in b.items()}
+
+
+@pytest.mark.parametrize("T", [24, 1400])
+def test_captured_step_replays(T):
+    """Every replay, with other eager work between them, equals the eager calls on the
+    buffers' contents of that time."""
+    shape = (T, 264, 136, 20, 8)
+    cfg = config("bf16", H=264, I=136, E=20, K=8)
+    b = step_buffers(1, *shape)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step_calls(cfg, b)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step_calls(cfg, b)
+    for seed in (1, 50, 90):
+        fresh = step_buffers(seed, *shape)
+        for k in b:
+            b[k].copy_(fresh[k])
+        g.replay()
+        torch.cuda.synchronize()
+        eager = step_calls(cfg, fresh)
+        step_calls(cfg, step_buffers(seed + 7, *shape))
+        torch.cuda.synchronize()
+        for i, (p, q) in enumerate(zip(out, eager)):
+            assert torch.equal(p, q), (seed, i)
+
+
+def test_streams_and_calls_at_once():
+    """Calls on two streams at once, each with its own temporaries, and the same inputs
+    again: equal bit for bit."""
+    shape = (1500, 264, 136, 20, 8)
+    cfg = config("bf16", H=264, I=136, E=20, K=8)
+    bufs = [step_buffers(s, *shape) for s in (3, 4)]
+    want = [step_calls(cfg, b) for b in bufs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(3):
+        for s, b in zip(streams, bufs):
+            with torch.cuda.stream(s):
+                got.append(step_calls(cfg, b))
+    torch.cuda.synchronize()
+    for n, outs in enumerate(got):
+        assert all(torch.equal(p, q) for p, q in zip(outs, want[n % 2])), n
+    # a stream passed beside the current one: temporaries belong to it
+    s = streams[0]
+    b = bufs[0]
+    rows = []
+    for _ in range(8):
+        rows.append(bm.beam_moe_sort(cfg, b["ids"], stream=s))
+        torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+        rows.append(bm.beam_moe_route_backward(cfg, b["x"], b["wr"], b["z"], b["ids"], b["w"], stream=s))
+    s.synchronize()
+    ref = bm.beam_moe_route_backward(cfg, b["x"], b["wr"], b["z"], b["ids"], b["w"])
+    torch.cuda.synchronize()
+    for n, r in enumerate(rows):
+        assert all(torch.equal(p, q) for p, q in zip(r, ref if n % 2 else want[0][:3]))
+
+
+def test_binding_refuses_wrong_tensors():
+    cfg = config("bf16", H=64, I=32, E=4, K=2)
+    ids = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    x = torch.zeros((3, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((3, 2), device="cuda")
+    off, row, pair = bm.beam_moe_sort(cfg, ids)
+    for bad in (ids.long(), ids[:, :1], torch.zeros((2, 3), dtype=torch.int32, device="cuda").t()):
+        with pytest.raises(ValueError):
+            bm.beam_moe_sort(cfg, bad)
+        with pytest.raises(ValueError):
+            bm.beam_moe_dispatch(cfg, x, bad)
+    for bad in (x.float(), x[:, :32], x.t().contiguous().t()):
+        with pytest.raises(ValueError):
+            bm.beam_moe_dispatch(cfg, bad, row)
+        with pytest.raises(ValueError):
+            bm.beam_moe_combine(cfg, bad, row, w)
+    with pytest.raises(ValueError):
+        bm.beam_moe_combine(cfg, x, row, w.double())
+    with pytest.raises(ValueError):
+        bm.beam_moe_combine(cfg, x, row.cpu(), w)
+    with pytest.raises(ValueError):
+        bm.beam_moe_swiglu(cfg, x, weights=w, row_of_pair=row, keep_q=torch.zeros(3, 64, device="cuda"),
+                           keep_scale=torch.zeros(3, 2, 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(bm.BeamMoEError):                   # a view that starts inside 16 bytes
+        bm.beam_moe_dispatch(cfg, torch.zeros(3 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(3, 64), row)
+    with pytest.raises(bm.BeamMoEError):                   # one row a token needs one pick
+        bm.beam_moe_dispatch(cfg, x, None)
+    with pytest.raises(bm.BeamMoEError):                   # the workspace is too small
+        bm.beam_moe_route_backward(cfg, x, torch.zeros((64, 4), device="cuda"), torch.zeros((3, 4), device="cuda"), ids, w,
+                                   ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()

@@ -1,0 +1,163 @@
+"""Refusals of the training operators at the C ABI, before anything is enqueued (no GPU):
+bad configs, missing or misaligned pointers, arguments that exclude each other, short
+workspaces, sizes past the 32-bit grids; and the calls with nothing to do."""
+import ctypes
+
+import pytest
+
+import sparse_mixture_experts_group_amd as bm
+
+P = ctypes.c_void_p(0x10000)        # never dereferenced: every call below ends on the host
+ODD = ctypes.c_void_p(0x10008)      # not 16-byte aligned
+BIG = 1 << 40
+OK, ARG, UNSUPPORTED, WS = bm.BEAM_OK, bm.BEAM_ERR_INVALID_ARG, bm.BEAM_ERR_UNSUPPORTED, bm.BEAM_ERR_WORKSPACE
+
+
+def cfg(**kw):
+    return bm.make_config(**{**dict(hidden=100, inter=50, n_experts=7, topk=3), **kw})
+
+
+def sort(c=None, T=4, ids=P, off=P, row=P, pair=P, ws=None, nb=0):
+    return bm.lib().beam_moe_sort(ctypes.byref(c or cfg()), T, ids, off, row, pair, ws, nb, None)
+
+
+def dispatch(c=None, T=4, x=P, xscale=None, row=P, rows=12, xs=P, q=None, scale=None):
+    return bm.lib().beam_moe_dispatch(ctypes.byref(c or cfg()), T, x, xscale, row, rows, xs, q, scale, None)
+
+
+def dispatch_backward(c=None, T=4, dxs=P, row=P, rows=12, dx=P):
+    return bm.lib().beam_moe_dispatch_backward(ctypes.byref(c or cfg()), T, dxs, row, rows, dx, None)
+
+
+def combine(c=None, T=4, eo=P, row=P, rows=12, w=P, y=P):
+    return bm.lib().beam_moe_combine(ctypes.byref(c or cfg()), T, eo, row, rows, w, y, None)
+
+
+def combine_backward(c=None, T=4, dy=P, eo=P, row=P, rows=12, w=P, deo=P, dw=P):
+    return bm.lib().beam_moe_combine_backward(ctypes.byref(c or cfg()), T, dy, eo, row, rows, w, deo, dw, None)
+
+
+def swiglu(c=None, T=4, gu=P, row=P, rows=12, w=P, h=P, q=None, scale=None):
+    return bm.lib().beam_moe_swiglu(ctypes.byref(c or cfg()), T, gu, row, rows, w, h, q, scale, None)
+
+
+def swiglu_backward(c=None, T=4, dh=P, gu=P, scale=None, row=P, rows=12, w=P, dgu=P, h=P, dw=P):
+    return bm.lib().beam_moe_swiglu_backward(ctypes.byref(c or cfg()), T, dh, gu, scale, row, rows, w, dgu, h, dw,
+                                             None)
+
+
+def route_backward(c=None, T=4, x=P, wr=P, z=P, ids=P, dw=P, add=None, dx=P, dwr=P, db=P, ws=P, nb=BIG):
+    return bm.lib().beam_moe_route_backward(ctypes.byref(c or cfg()), T, x, wr, z, ids, dw, add, dx, dwr, db, ws, nb,
+                                            None)
+
+
+ALL = [sort, dispatch, dispatch_backward, combine, combine_backward, swiglu, swiglu_backward, route_backward]
+ROWS = [dispatch, dispatch_backward, combine, combine_backward, swiglu, swiglu_backward]
+
+
+@pytest.mark.parametrize("call", ALL)
+def test_bad_configs_and_counts(call):
+    assert call(cfg(topk=0)) == ARG
+    assert call(cfg(topk=33)) == ARG
+    assert call(T=-1) == ARG
+    assert call(cfg(topk=32), T=1 << 26) == ARG            # pairs past INT32_MAX / 2
+    if call is not sort:
+        c = cfg(**{"inter" if "swiglu" in call.__name__ else "hidden": 0})
+        assert call(c) == ARG
+        assert call(cfg(act_dtype=9)) == ARG
+        assert call(cfg(act_dtype=bm.BEAM_DTYPE_FP8_E4M3)) == UNSUPPORTED
+        wide = cfg(hidden=1 << 30, inter=1 << 29)
+        assert call(wide, T=1 << 20) == ARG                # an array of 2^50 elements
+    fn = getattr(bm.lib(), "beam_moe_" + call.__name__)
+    args = [0 if t is not ctypes.c_void_p else None for t in fn.argtypes[2:]]
+    assert fn(None, 4, *args) == ARG                       # no configuration
+
+
+@pytest.mark.parametrize("call", ROWS)
+def test_rows_out_of_range(call):
+    assert call(rows=-1) == ARG
+    assert call(rows=1 << 31) == ARG
+    assert call(cfg(hidden=1 << 20, inter=1 << 20), rows=1 << 30) == ARG
+
+
+def test_experts_out_of_range():
+    for call in (sort, route_backward):
+        assert call(cfg(n_experts=0)) == ARG
+        assert call(cfg(n_experts=257)) == ARG
+    assert bm.beam_moe_sort_workspace_size(cfg(n_experts=257), 4) == 0
+    assert bm.beam_moe_route_backward_workspace_size(cfg(n_experts=0), 4) == 0
+
+
+def test_sort_arguments():
+    for k in ("ids", "off", "row", "pair"):
+        assert sort(**{k: None}) == ARG and sort(**{k: ODD}) == ARG
+    assert sort(T=0, off=None) == ARG                      # the offsets of no pairs are written
+    big = 8192 // 3 + 1
+    need = bm.beam_moe_sort_workspace_size(cfg(), big)
+    assert bm.beam_moe_sort_workspace_size(cfg(), 8192 // 3) == 0 and need > 0
+    assert sort(T=big) == WS
+    assert sort(T=big, ws=P, nb=need - 1) == WS
+    assert sort(T=big, ws=ODD, nb=need) == ARG
+
+
+def test_dispatch_arguments():
+    for k in ("x", "row"):
+        assert dispatch(**{k: None}) == ARG and dispatch(**{k: ODD}) == ARG     # row NULL needs topk 1
+    assert dispatch(xs=None) == ARG                        # neither rows nor a copy
+    assert dispatch(xs=ODD) == ARG and dispatch(xscale=ODD) == ARG
+    assert dispatch(q=P) == ARG and dispatch(scale=P) == ARG                    # both or neither
+    assert dispatch(q=P, scale=P, xscale=P) == ARG         # a copy of a copy
+    assert dispatch(q=ODD, scale=P) == ARG and dispatch(q=P, scale=ODD) == ARG
+    assert dispatch(T=0, x=None, row=P, xs=None) == OK
+    assert dispatch(rows=0, xs=None) == OK                 # no row to write
+
+
+def test_combine_arguments():
+    for call, names in ((dispatch_backward, ("dxs", "row", "dx")), (combine, ("eo", "row", "w", "y")),
+                        (combine_backward, ("dy", "row", "w", "deo"))):
+        for k in names:
+            assert call(**{k: None}) == ARG and call(**{k: ODD}) == ARG, (call, k)
+        assert call(T=0, **{k: None for k in names}) == OK
+    assert combine_backward(eo=None) == ARG and combine_backward(dw=None) == ARG     # both or neither
+
+
+def test_swiglu_arguments():
+    for k in ("gu", "h", "row"):
+        assert swiglu(**{k: None}) == ARG and swiglu(**{k: ODD}) == ARG
+    for k in ("dh", "gu", "dgu", "row"):
+        assert swiglu_backward(**{k: None}) == ARG and swiglu_backward(**{k: ODD}) == ARG
+    assert swiglu(w=ODD) == ARG and swiglu_backward(w=ODD) == ARG
+    assert swiglu(q=P) == ARG and swiglu(scale=P) == ARG
+    assert swiglu(q=P, scale=ODD) == ARG
+    for k in ("h", "scale", "dw"):
+        assert swiglu_backward(**{k: ODD}) == ARG
+    assert swiglu_backward(w=None) == ARG                  # gradients of weights that are not there
+    assert swiglu(T=0) == OK and swiglu(rows=0, gu=None, h=None) == OK
+    assert swiglu_backward(T=0, dh=None, gu=None, dgu=None) == OK
+
+
+def test_route_backward_arguments():
+    for k in ("x", "wr", "z", "ids", "dw", "dwr"):
+        assert route_backward(**{k: None}) == ARG and route_backward(**{k: ODD}) == ARG, k
+    for k in ("add", "dx", "db"):
+        assert route_backward(**{k: ODD}) == ARG
+    assert route_backward(add=P, dx=None) == ARG
+    assert route_backward(cfg(routed_scale=float("inf"))) == ARG
+    assert route_backward(cfg(hidden=(1 << 20) + 1)) == UNSUPPORTED
+    need = bm.beam_moe_route_backward_workspace_size(cfg(), 4)
+    assert need > 0
+    assert route_backward(ws=None) == WS and route_backward(nb=need - 1) == WS and route_backward(ws=ODD) == ARG
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    c = cfg()
+    ids = torch.zeros(4, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        bm.beam_moe_sort(c, ids)
+    with pytest.raises(ValueError, match="two dimensions"):
+        bm.beam_moe_sort(c, ids.reshape(-1))
+    with pytest.raises(ValueError, match="GPU"):
+        bm.beam_moe_dispatch(c, torch.zeros(4, 100, dtype=torch.bfloat16), ids)
+    with pytest.raises(bm.BeamMoEError):
+        bm.beam_moe_dispatch(cfg(act_dtype=bm.BEAM_DTYPE_FP8_E4M3), torch.zeros(4, 100), ids)
