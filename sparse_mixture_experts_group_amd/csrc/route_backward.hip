@@ -9,30 +9,51 @@ namespace beam {
 
 namespace {
 
-constexpr int kColTile = 128;      // hidden columns of one block
+constexpr int kColTile = 128;      // hidden columns of a dx block
 constexpr int kDxStride = kColTile + 2;
-constexpr int kDwStride = kColTile + 1;
+constexpr int kDwTokens = 32;      // tokens of one stage of a dW block
+constexpr int kDwAhead = 4;        // stages in flight (even: the buffers alternate)
 constexpr int kCUs = 256;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Experts (padded) and hidden columns of a dW block.
+int dw_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
+int dw_cols(int E) { return E <= 64 ? 256 : 128; }
+
+// Ranges that T tokens are cut into so that `tiles` blocks a range fill the chip, a range
+// no shorter than `least` tokens.
+int token_splits(int64_t T, int64_t tiles, int least) {
+    int64_t s = kCUs / tiles;
+    if (s > (T + least - 1) / least) s = (T + least - 1) / least;
+    return static_cast<int>(s < 1 ? 1 : s);
+}
 
 }  // namespace
 
 RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K) {
     RouteBackwardPlan p;
-    const int64_t tiles = (static_cast<int64_t>(H) + 1 + kColTile - 1) / kColTile;   // a column for the bias
-    int64_t s = kCUs / tiles;
-    if (s > (T + 63) / 64) s = (T + 63) / 64;
-    if (s < 1) s = 1;
-    if (T == 0) s = 0;
-    p.splits = static_cast<int>(s);
+    const int nt = dw_cols(E);
+    const int64_t tiles = (static_cast<int64_t>(H) + 1 + nt - 1) / nt;       // a column for the bias
+    p.splits = T == 0 ? 0 : token_splits(T, tiles, 2 * kDwTokens);
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += align256(bytes); return o; };
     p.dz = take(sizeof(float) * T * K);
     p.expert = take(sizeof(int32_t) * T * K);
+    p.split = take(8 * T * K);
+    p.live = take(T + 4);                      // read four at a time
     p.part = take(sizeof(float) * p.splits * (static_cast<size_t>(H) + 1) * E);
     p.total = off;
     return p;
+}
+
+// An FP32 value as the sum of three BF16 values, 8 bits each: each remainder is exact.
+__device__ __forceinline__ void split3(float v, uint16_t* s) {
+    s[0] = f32_to_bf16_bits(v);
+    v -= bf16_bits_to_f32(s[0]);
+    s[1] = f32_to_bf16_bits(v);
+    v -= bf16_bits_to_f32(s[1]);
+    s[2] = f32_to_bf16_bits(v);
 }
 
 // ---------------------------------------------------------------------------
@@ -40,11 +61,15 @@ RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K) {
 //   dz_i = alpha p_i (1 - s_i) sum_j p_j (g_i - g_j),
 // g the weights' gradients.  The sum over differences loses nothing when the g are nearly
 // equal, and 1 - s_i = sigma(-z_i) nothing when s_i is near one.  A lane a pick, `group`
-// lanes (a power of two, at least K) a token.  An id outside [0, E) is no pick.
+// lanes (a power of two, at least K) a token.  An id outside [0, E) is no pick.  Picks of
+// one expert by the same token are joined in the first of them, and a token without picks
+// is marked, so that what follows meets each (token, expert) once and reads no other x.
+// split: a pick's dz as three BF16 values and its expert (0xFFFF: none), for dW.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void route_dz(RouteBackwardArgs a, int group, const float* __restrict__ logits,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ dweights,
-                                                float* __restrict__ dz, int32_t* __restrict__ expert) {
+                                                float* __restrict__ dz, int32_t* __restrict__ expert,
+                                                uint16_t* __restrict__ split, uint8_t* __restrict__ alive) {
     const int64_t g0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t t = g0 / group;
     const int i = static_cast<int>(threadIdx.x) & (group - 1);
@@ -60,107 +85,397 @@ __global__ __launch_bounds__(256) void route_dz(RouteBackwardArgs a, int group, 
     const float p = live ? s / d : 0.0f;
     float sum = 0.0f;
     for (int k = 0; k < a.K; ++k) sum = fmaf(__shfl(p, base + k, kWave), g - __shfl(g, base + k, kWave), sum);
+    const float v = live ? a.alpha * p * router_sigmoid(-z) * sum : 0.0f;
+    float joined = 0.0f;
+    bool first = live;
+    for (int k = 0; k < a.K; ++k) {
+        const bool same = __shfl(e, base + k, kWave) == e;
+        joined += same ? __shfl(v, base + k, kWave) : 0.0f;
+        first = first && !(same && k < i);
+    }
     if (here) {
-        dz[t * a.K + i] = live ? a.alpha * p * router_sigmoid(-z) * sum : 0.0f;
-        expert[t * a.K + i] = live ? e : -1;
+        dz[t * a.K + i] = first ? joined : 0.0f;
+        expert[t * a.K + i] = first ? e : -1;
+        uint16_t q[3];
+        split3(joined, q);
+        *reinterpret_cast<u32x2*>(split + (t * a.K + i) * 4) =
+            u32x2{q[0] | (static_cast<uint32_t>(q[1]) << 16), q[2] | (first ? static_cast<uint32_t>(e) << 16 : 0xFFFF0000u)};
     }
+    const uint64_t any = wave_ballot(first) >> base;
+    if (here && i == 0) alive[t] = (any & ((1ull << group) - 1)) != 0;
 }
 
-// Two columns of a row at element i; n of them exist.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Row t of an activation array (t is the same for the whole wave: a scalar address).
 template <bool BF16>
-__device__ __forceinline__ void load2(const void* base, int64_t i, int n, float* v) {
-    if constexpr (BF16) {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + i;
-        v[0] = n > 0 ? bf16_bits_to_f32(p[0]) : 0.0f;
-        v[1] = n > 1 ? bf16_bits_to_f32(p[1]) : 0.0f;
+__device__ __forceinline__ const void* row_at(const void* base, int64_t t, int H) {
+    return static_cast<const char*>(base) + t * H * (BF16 ? 2 : 4);
+}
+
+// Columns c, c + 1 of a row (c even) as stored: two BF16 in one word, or two FP32.  Those
+// past the row come out as 0.  EVEN: H is even, so a pair lies in the row or behind it and
+// is one load.  Every lane loads (clamped into the row): the loads of several rows stay in
+// flight without branches between them.
+template <bool BF16>
+struct Pair {
+    uint32_t w[BF16 ? 1 : 2];
+    __device__ __forceinline__ f32x2 wide() const {
+        if constexpr (BF16) return f32x2{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u)};
+        else return f32x2{__uint_as_float(w[0]), __uint_as_float(w[1])};
+    }
+};
+
+template <bool BF16, bool EVEN>
+__device__ __forceinline__ Pair<BF16> load2(const void* row, uint32_t H, uint32_t c) {
+    Pair<BF16> p;
+    if constexpr (EVEN) {
+        const uint32_t at = c < H ? c / 2 : 0;
+        if constexpr (BF16) {
+            const uint32_t d = static_cast<const uint32_t*>(row)[at];
+            p.w[0] = c < H ? d : 0;
+        } else {
+            const u32x2 d = static_cast<const u32x2*>(row)[at];
+            p.w[0] = c < H ? d[0] : 0;
+            p.w[1] = c < H ? d[1] : 0;
+        }
     } else {
-        const float* p = static_cast<const float*>(base) + i;
-        v[0] = n > 0 ? p[0] : 0.0f;
-        v[1] = n > 1 ? p[1] : 0.0f;
+        const uint32_t a0 = c < H ? c : 0, a1 = c + 1 < H ? c + 1 : 0;
+        if constexpr (BF16) {
+            const uint32_t lo = static_cast<const uint16_t*>(row)[a0], hi = static_cast<const uint16_t*>(row)[a1];
+            p.w[0] = (c < H ? lo : 0) | (c + 1 < H ? hi << 16 : 0);
+        } else {
+            const uint32_t lo = static_cast<const uint32_t*>(row)[a0], hi = static_cast<const uint32_t*>(row)[a1];
+            p.w[0] = c < H ? lo : 0;
+            p.w[1] = c + 1 < H ? hi : 0;
+        }
+    }
+    return p;
+}
+
+template <bool BF16, bool EVEN>
+__device__ __forceinline__ void store2(void* row, uint32_t H, uint32_t c, f32x2 v) {
+    if constexpr (EVEN) {
+        if (c >= H) return;
+        if constexpr (BF16)
+            static_cast<uint32_t*>(row)[c / 2] = static_cast<uint32_t>(f32_to_bf16_bits(v[0])) |
+                                                 (static_cast<uint32_t>(f32_to_bf16_bits(v[1])) << 16);
+        else static_cast<f32x2*>(row)[c / 2] = v;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (c + k >= H) continue;
+            if constexpr (BF16) static_cast<uint16_t*>(row)[c + k] = f32_to_bf16_bits(v[k]);
+            else static_cast<float*>(row)[c + k] = v[k];
+        }
     }
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store1(void* base, int64_t i, float v) {
-    if constexpr (BF16) static_cast<uint16_t*>(base)[i] = f32_to_bf16_bits(v);
-    else static_cast<float*>(base)[i] = v;
+__device__ __forceinline__ float lane_float(float v, int l) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
 }
 
 // ---------------------------------------------------------------------------
 // dx[t] = dx_add[t] + sum_i dz_i W[:, e_i], FP32, one rounding.  A block holds 128 columns
 // of W for all experts in LDS (expert-major, 130 KB for 256 experts: one block a CU) and
-// walks its tokens, a wave a token, two columns a lane: K reads of 512 bytes a token
-// instead of a dense product over E.
+// walks its tokens, two columns a lane: K reads of 512 bytes a token instead of a dense
+// product over E.  A wave takes up to 8 tokens at a time (64 picks, a pick a lane); the
+// picks and addends of its next tokens are loaded before it works on these.
 // ---------------------------------------------------------------------------
-template <bool BF16>
+template <bool BF16, bool EVEN, int KT, bool ADD>
 __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t per_split, const float* __restrict__ wr,
                                                  const float* __restrict__ dz, const int32_t* __restrict__ expert,
                                                  const void* dx_add, void* dx) {
-    extern __shared__ float s_w[];
+    extern __shared__ __attribute__((aligned(16))) float s_w[];
     const int c0 = blockIdx.x * kColTile;
-    const int cols = a.H - c0 < kColTile ? a.H - c0 : kColTile;
-    for (int j = threadIdx.x; j < cols * a.E; j += 1024) {
-        const int c = j / a.E, e = j - c * a.E;
-        s_w[e * kDxStride + c] = wr[static_cast<int64_t>(c0) * a.E + j];
+    const int size = (a.H - c0 < kColTile ? a.H - c0 : kColTile) * a.E;
+    const float* w0 = wr + static_cast<int64_t>(c0) * a.E;
+    for (int j0 = threadIdx.x; j0 < size; j0 += 8 * 1024) {      // eight loads in flight
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = w0[j0 + 1024 * k < size ? j0 + 1024 * k : 0];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int j = j0 + 1024 * k, col = j / a.E;
+            if (j < size) s_w[(j - col * a.E) * kDxStride + col] = v[k];
+        }
     }
     __syncthreads();
+    const int K = KT > 0 ? KT : a.K;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t1 = per_split * (blockIdx.y + 1) < a.T ? per_split * (blockIdx.y + 1) : a.T;
-    const int c = c0 + lane * 2, n = a.H - c;
-    for (int64_t t = per_split * blockIdx.y + wave; t < t1; t += 16) {
-        float acc[2] = {0.0f, 0.0f};
-        if (dx_add && n > 0) load2<BF16>(dx_add, t * a.H + c, n, acc);
-        for (int i = 0; i < a.K; ++i) {
-            const int e = expert[t * a.K + i];
-            const float v = dz[t * a.K + i];
-            if (e >= 0) {
-                const float* w = s_w + e * kDxStride + lane * 2;
-                acc[0] = fmaf(v, w[0], acc[0]);
-                acc[1] = fmaf(v, w[1], acc[1]);
+    const int batch = KT > 0 ? 8 : (K <= 8 ? 8 : 64 / K);       // tokens a wave takes at a time
+    const int64_t t0 = per_split * blockIdx.y;
+    const int64_t t1 = t0 + per_split < a.T ? t0 + per_split : a.T;
+    const int c = c0 + lane * 2;
+    const int64_t last = t1 * K - 1;
+    int e_next = -1;
+    float v_next = 0.0f;
+    Pair<BF16> add_next[8];
+    f32x2 add[8];
+    auto fetch = [&](int64_t t) {
+        const int64_t p = t * K + lane < last ? t * K + lane : last;
+        e_next = expert[p];
+        v_next = dz[p];
+        if constexpr (ADD) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) add_next[j] = load2<BF16, EVEN>(row_at<BF16>(dx_add, t + j < t1 ? t + j : t1 - 1, a.H), a.H, c);
+        }
+    };
+    int64_t t = t0 + static_cast<int64_t>(wave) * batch;
+    if (t < t1) fetch(t);
+    for (; t < t1; t += 16 * batch) {
+        // no pick: expert 0 with factor 0 (the router's weights are finite)
+        const int at = (e_next > 0 ? e_next : 0) * (kDxStride / 2);
+        const float v = e_next >= 0 ? v_next : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add[j] = ADD ? add_next[j].wide() : f32x2{0.0f, 0.0f};
+        if (t + 16 * batch < t1) fetch(t + 16 * batch);
+        const f32x2* mine = reinterpret_cast<const f32x2*>(s_w) + lane;
+        auto pick = [&](int l, f32x2& acc) {
+            const float f = lane_float(v, l);
+            const f32x2 w = mine[__builtin_amdgcn_readlane(at, l)];
+            acc[0] = fmaf(f, w[0], acc[0]);
+            acc[1] = fmaf(f, w[1], acc[1]);
+        };
+        const int m = t1 - t < batch ? static_cast<int>(t1 - t) : batch;
+        if (KT > 0 && m == 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) pick(j * KT + i, add[j]);
+                store2<BF16, EVEN>(const_cast<void*>(row_at<BF16>(dx, t + j, a.H)), a.H, c, add[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j < m) {
+                    for (int i = 0; i < K; ++i) pick(j * K + i, add[j]);
+                    store2<BF16, EVEN>(const_cast<void*>(row_at<BF16>(dx, t + j, a.H)), a.H, c, add[j]);
+                }
             }
         }
-        if (n > 0) store1<BF16>(dx, t * a.H + c, acc[0]);
-        if (n > 1) store1<BF16>(dx, t * a.H + c + 1, acc[1]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// dW[h, e] = sum_t x[t, h] dz[t, e], and the bias' gradient as column h = H with x = 1.
-// A block holds the sums of 128 columns and all experts in LDS; each column belongs to one
-// lane, so an LDS add meets no other lane's and the order is that of the tokens.  Token
-// ranges (blockIdx.y) write partial sums.
+// dW[h, e] = sum_t x[t, h] dz[t, e], and the bias' gradient as column h = H with x = 1, on
+// the matrix cores with the tokens as the summed index.  An FP32 value is the sum of three
+// BF16 values (8 bits each, cut off by rounding to nearest: the rest is exact), so dz is
+// three operands, and x is one (BF16) or three (FP32, where the six products of largest
+// order are kept: the others are under 2^-24 of the result's terms).  Sums in FP32.
+//
+// A block: ME experts x NT columns, eight waves of 64 experts x NW columns (32 x 32 x 16
+// products).  A stage of 32 tokens lies in LDS as rows of 64 bytes (one expert or column,
+// 32 tokens): x is transposed in registers on its way in, dz is scattered (at most K
+// entries a token) into rows that hold zeros, and its entries are taken out again before
+// the buffer's next stage.  Two buffers: a stage's loads are in flight during the products
+// of the stage before it.  Token ranges (blockIdx.y) write partial sums [H+1, E].
 // ---------------------------------------------------------------------------
-template <bool BF16>
-__global__ __launch_bounds__(128) void route_dw(RouteBackwardArgs a, int64_t per_split, const void* __restrict__ x,
-                                                const float* __restrict__ dz, const int32_t* __restrict__ expert,
+template <bool BF16, int ME>
+struct DwTile {
+    static constexpr int WM = ME / 64, WN = 8 / WM;
+    static constexpr int NW = ME == 256 ? 64 : 32, NT = WN * NW, TN = NW / 32;
+    static constexpr int XS = BF16 ? 1 : 3;
+    static constexpr int kRows = 3 * ME + XS * NT;       // LDS rows of a stage
+    static constexpr int kLds = 2 * kRows * kStageRowBytes;
+};
+
+template <bool BF16, bool EVEN, int ME>
+__global__ __launch_bounds__(512) void route_dw(RouteBackwardArgs a, int64_t per_split, const void* __restrict__ x,
+                                                const u32x2* __restrict__ split, const uint8_t* __restrict__ alive,
                                                 float* __restrict__ part) {
-    extern __shared__ float s_acc[];
-    for (int j = threadIdx.x; j < a.E * kDwStride; j += 128) s_acc[j] = 0.0f;
-    __syncthreads();
-    const int c0 = blockIdx.x * kColTile;
-    const int col = threadIdx.x, c = c0 + col;
+    using L = DwTile<BF16, ME>;
+    extern __shared__ __attribute__((aligned(16))) char s_stage[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % L::WM, wn = wave / L::WM;
+    const int c0 = blockIdx.x * L::NT;
+    const bool edge = c0 + L::NT > a.H;        // the tile holds the bias' column
     const int64_t t0 = per_split * blockIdx.y;
     const int64_t t1 = t0 + per_split < a.T ? t0 + per_split : a.T;
-    for (int64_t t = t0; t < t1; ++t) {
-        float v = 1.0f;
-        if (c < a.H) {
-            if constexpr (BF16) v = bf16_bits_to_f32(static_cast<const uint16_t*>(x)[t * a.H + c]);
-            else v = static_cast<const float*>(x)[t * a.H + c];
+    for (int j = tid; j < L::kLds / 16; j += 512) reinterpret_cast<u32x4*>(s_stage)[j] = u32x4{0, 0, 0, 0};
+
+    constexpr int NP = L::NT / 128;            // column pairs of a lane
+    struct Stage {
+        Pair<BF16> x[NP][4];                   // a lane's columns of its wave's four tokens
+        uint32_t live;                         // a byte each
+        u32x2 pick[2];                         // a thread's picks
+    } ahead[kDwAhead];
+    // thread -> up to two of the stage's 32 K picks, and the token's place in an LDS row
+    const int picks = kDwTokens * a.K;
+    const bool two = picks > 512;
+    int chunk[2], byte[2], old[2][2] = {{-1, -1}, {-1, -1}};     // old: LDS places per buffer
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int tok = (tid + 512 * q) / a.K;
+        chunk[q] = tok >> 3;
+        byte[q] = (tok & 7) * 2;
+    }
+    const int64_t last = t1 * a.K - 1;
+    auto fetch = [&](Stage& f, int64_t t) {
+        const int64_t tw = t + wave * 4;
+        f.live = *reinterpret_cast<const uint32_t*>(alive + (tw < t1 ? tw : t0));   // tw is a multiple of 4
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const void* row = row_at<BF16>(x, tw + j < t1 ? tw + j : t1 - 1, a.H);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) f.x[q][j] = load2<BF16, EVEN>(row, a.H, c0 + q * 128 + lane * 2);
         }
-        for (int i = 0; i < a.K; ++i) {
-            const int e = expert[t * a.K + i];
-            if (e >= 0)
-                __hip_atomic_fetch_add(&s_acc[e * kDwStride + col], v * dz[t * a.K + i], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_WORKGROUP);
+        const int64_t p0 = t * a.K + tid;
+        f.pick[0] = split[p0 < last ? p0 : last];
+        if (two) f.pick[1] = split[p0 + 512 < last ? p0 + 512 : last];
+    };
+    auto clear = [&](int b) {
+        char* s = s_stage + b * L::kRows * kStageRowBytes;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if ((q == 0 || two) && old[b][q] >= 0) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint16_t*>(s + k * ME * kStageRowBytes + old[b][q]) = 0;
+            }
         }
+    };
+    auto fill_dz = [&](int b, const Stage& f, int64_t t) {
+        char* s = s_stage + b * L::kRows * kStageRowBytes;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (q == 1 && !two) continue;
+            const int i = tid + 512 * q, e = f.pick[q][1] >> 16;
+            old[b][q] = -1;
+            if (i < picks && t * a.K + i <= last && e != 0xFFFF) {
+                old[b][q] = stage_offset(e, chunk[q]) + byte[q];
+                *reinterpret_cast<uint16_t*>(s + old[b][q]) = static_cast<uint16_t>(f.pick[q][0]);
+                *reinterpret_cast<uint16_t*>(s + ME * kStageRowBytes + old[b][q]) =
+                    static_cast<uint16_t>(f.pick[q][0] >> 16);
+                *reinterpret_cast<uint16_t*>(s + 2 * ME * kStageRowBytes + old[b][q]) =
+                    static_cast<uint16_t>(f.pick[q][1]);
+            }
+        }
+    };
+    auto fill_x = [&](int b, const Stage& f, int64_t t) {
+        char* sx = s_stage + (b * L::kRows + 3 * ME) * kStageRowBytes;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const int col = q * 128 + lane * 2;
+            Pair<BF16> v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // a token without picks is not looked at
+                const bool in = ((f.live >> (8 * j)) & 0xff) && t + wave * 4 + j < t1;
+#pragma unroll
+                for (int k = 0; k < (BF16 ? 1 : 2); ++k) v[j].w[k] = in ? f.x[q][j].w[k] : 0;
+                if (edge) {                    // the bias' column is ones
+                    if constexpr (BF16) {
+                        v[j].w[0] |= c0 + col == a.H ? 0x3F80u : c0 + col + 1 == a.H ? 0x3F800000u : 0u;
+                    } else {
+                        v[j].w[0] |= c0 + col == a.H ? 0x3F800000u : 0u;
+                        v[j].w[1] |= c0 + col + 1 == a.H ? 0x3F800000u : 0u;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {      // a column: four tokens, 8 bytes
+                char* to = sx + stage_offset(col + k, wave >> 1) + (wave & 1) * 8;
+                if constexpr (BF16) {
+                    const uint32_t sel = k == 0 ? 0x05040100u : 0x07060302u;      // low or high halves
+                    *reinterpret_cast<u32x2*>(to) = u32x2{__builtin_amdgcn_perm(v[1].w[0], v[0].w[0], sel),
+                                                          __builtin_amdgcn_perm(v[3].w[0], v[2].w[0], sel)};
+                } else {
+                    uint16_t p[4][3];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) split3(__uint_as_float(v[j].w[k]), p[j]);
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        *reinterpret_cast<u32x2*>(to + m * L::NT * kStageRowBytes) =
+                            u32x2{p[0][m] | (static_cast<uint32_t>(p[1][m]) << 16),
+                                  p[2][m] | (static_cast<uint32_t>(p[3][m]) << 16)};
+                }
+            }
+        }
+    };
+
+    f32x16 acc[2][L::TN] = {};
+    auto products = [&](int b) {
+        const char* s = s_stage + b * L::kRows * kStageRowBytes;
+        const char* sx = s + 3 * ME * kStageRowBytes;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const int chunk = ks * 2 + (lane >> 5);
+            bf16x8 fz[2][3], fx[L::TN][L::XS];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    fz[i][k] = *reinterpret_cast<const bf16x8*>(
+                        s + k * ME * kStageRowBytes + stage_offset(wm * 64 + i * 32 + (lane & 31), chunk));
+#pragma unroll
+            for (int i = 0; i < L::TN; ++i)
+#pragma unroll
+                for (int k = 0; k < L::XS; ++k)
+                    fx[i][k] = *reinterpret_cast<const bf16x8*>(
+                        sx + k * L::NT * kStageRowBytes + stage_offset(wn * L::NW + i * 32 + (lane & 31), chunk));
+#pragma unroll
+            for (int order = 2; order >= 0; --order)     // small products first
+#pragma unroll
+                for (int k = 0; k < L::XS; ++k)
+                    if (order - k >= 0) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < L::TN; ++j)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fz[i][order - k], fx[j][k],
+                                                                                   acc[i][j], 0, 0, 0);
+                    }
+        }
+    };
+
+    __syncthreads();
+    if (t0 < t1) {
+        static_for<0, kDwAhead>([&](auto u) { fetch(ahead[u], t0 + u * kDwTokens); });
+        fill_x(0, ahead[0], t0);
+        fill_dz(0, ahead[0], t0);
     }
     __syncthreads();
-    const int cols = a.H + 1 - c0 < kColTile ? a.H + 1 - c0 : kColTile;
-    float* out = part + (static_cast<int64_t>(blockIdx.y) * (a.H + 1) + c0) * a.E;
-    for (int j = threadIdx.x; j < cols * a.E; j += 128) {
-        const int cc = j / a.E, e = j - cc * a.E;
-        out[j] = s_acc[e * kDwStride + cc];
+    for (int64_t t = t0; t < t1; t += kDwAhead * kDwTokens) {
+        static_for<0, kDwAhead>([&](auto u) {
+            constexpr int b = u & 1, next = (u + 1) % kDwAhead;
+            const int64_t tu = t + u * kDwTokens;
+            if (tu >= t1) return;
+            const bool more = tu + kDwTokens < t1;
+            fetch(ahead[u], tu + kDwAhead * kDwTokens);          // its values lie in the buffer
+            // the other buffer's products are done (the barriers below): its entries go, and
+            // its columns come
+            clear(b ^ 1);
+            if (more) fill_x(b ^ 1, ahead[next], tu + kDwTokens);
+            products(b);
+            lds_pipeline_barrier();            // every entry is out before a new one goes in
+            if (more) fill_dz(b ^ 1, ahead[next], tu + kDwTokens);
+            lds_pipeline_barrier();
+        });
+    }
+
+    // lane: column n = lane % 32 of its tile, experts 8 (r / 4) + 4 (lane / 32) + r % 4
+#pragma unroll
+    for (int j = 0; j < L::TN; ++j) {
+        const int c = c0 + wn * L::NW + j * 32 + (lane & 31);
+        if (c > a.H) continue;
+        float* out = part + (static_cast<int64_t>(blockIdx.y) * (a.H + 1) + c) * a.E;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int e = wm * 64 + i * 32 + 2 * r + 4 * (lane >> 5);
+                const f32x4 v = {acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+                if (a.E % 4 == 0) {
+                    if (e < a.E) *reinterpret_cast<f32x4*>(out + e) = v;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (e + k < a.E) out[e + k] = v[k];
+                }
+            }
     }
 }
 
@@ -176,36 +491,59 @@ __global__ __launch_bounds__(256) void route_dw_sum(int64_t n, int64_t slice, in
     else if (dbias) dbias[i - bias_at] = v;
 }
 
-template <bool BF16>
+template <bool BF16, bool EVEN, int KT>
+static void dx_launch(hipStream_t st, const RouteBackwardArgs& a, const float* w_router, const float* dz,
+                      const int32_t* expert, const void* dx_add, void* dx) {
+    const int tiles = (a.H + kColTile - 1) / kColTile;
+    const int splits = token_splits(a.T, tiles, 64);
+    const int64_t per = (a.T + splits - 1) / splits;
+    const auto kernel = dx_add ? &route_dx<BF16, EVEN, KT, true> : &route_dx<BF16, EVEN, KT, false>;
+    lds_opt_in(reinterpret_cast<const void*>(kernel), sizeof(float) * kMaxExperts * kDxStride);
+    kernel<<<dim3(tiles, splits), 1024, sizeof(float) * a.E * kDxStride, st>>>(a, per, w_router, dz, expert, dx_add, dx);
+}
+
+template <bool BF16, bool EVEN, int ME>
+static void dw_launch(hipStream_t st, const RouteBackwardArgs& a, int splits, const void* x, const u32x2* split,
+                      const uint8_t* alive, float* part) {
+    using L = DwTile<BF16, ME>;
+    const int64_t per = ((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens;
+    lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16, EVEN, ME>), L::kLds);
+    route_dw<BF16, EVEN, ME><<<dim3((a.H + 1 + L::NT - 1) / L::NT, splits), 512, L::kLds, st>>>(a, per, x, split,
+                                                                                               alive, part);
+}
+
+template <bool BF16, bool EVEN>
 static void route_backward_typed(hipStream_t st, const RouteBackwardArgs& a, const RouteBackwardPlan& p, const void* x,
                                  const float* w_router, const void* dx_add, void* dx, const float* dz,
-                                 const int32_t* expert, float* part) {
-    const int64_t per = (a.T + p.splits - 1) / p.splits;
+                                 const int32_t* expert, const u32x2* split, const uint8_t* alive, float* part) {
     if (dx) {
-        const unsigned tiles = static_cast<unsigned>((a.H + kColTile - 1) / kColTile);
-        const int lds = static_cast<int>(sizeof(float)) * a.E * kDxStride;
-        lds_opt_in(reinterpret_cast<const void*>(&route_dx<BF16>), sizeof(float) * kMaxExperts * kDxStride);
-        route_dx<BF16><<<dim3(tiles, p.splits), 1024, lds, st>>>(a, per, w_router, dz, expert, dx_add, dx);
+        if (a.K == 8) dx_launch<BF16, EVEN, 8>(st, a, w_router, dz, expert, dx_add, dx);
+        else dx_launch<BF16, EVEN, 0>(st, a, w_router, dz, expert, dx_add, dx);
     }
-    const unsigned tiles = static_cast<unsigned>((a.H + 1 + kColTile - 1) / kColTile);
-    const int lds = static_cast<int>(sizeof(float)) * a.E * kDwStride;
-    lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16>), sizeof(float) * kMaxExperts * kDwStride);
-    route_dw<BF16><<<dim3(tiles, p.splits), 128, lds, st>>>(a, per, x, dz, expert, part);
+    const int me = dw_experts(a.E);
+    if (me == 64) dw_launch<BF16, EVEN, 64>(st, a, p.splits, x, split, alive, part);
+    else if (me == 128) dw_launch<BF16, EVEN, 128>(st, a, p.splits, x, split, alive, part);
+    else dw_launch<BF16, EVEN, 256>(st, a, p.splits, x, split, alive, part);
 }
 
 void launch_route_backward(hipStream_t st, const RouteBackwardArgs& a, const RouteBackwardPlan& p, const void* x,
                            const float* w_router, const float* logits, const int32_t* ids, const float* dweights,
                            const void* dx_add, void* dx, float* dw_router, float* dlogit_bias, void* ws) {
-    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+    char* base = static_cast<char*>(ws);
+    float* part = reinterpret_cast<float*>(base + p.part);
     if (a.T > 0) {
-        float* dz = reinterpret_cast<float*>(static_cast<char*>(ws) + p.dz);
-        int32_t* expert = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.expert);
+        float* dz = reinterpret_cast<float*>(base + p.dz);
+        int32_t* expert = reinterpret_cast<int32_t*>(base + p.expert);
+        uint16_t* split = reinterpret_cast<uint16_t*>(base + p.split);
+        uint8_t* alive = reinterpret_cast<uint8_t*>(base + p.live);
         int group = 1;
         while (group < a.K) group *= 2;
         route_dz<<<static_cast<unsigned>((a.T * group + 255) / 256), 256, 0, st>>>(a, group, logits, ids, dweights, dz,
-                                                                                  expert);
-        if (a.bf16) route_backward_typed<true>(st, a, p, x, w_router, dx_add, dx, dz, expert, part);
-        else route_backward_typed<false>(st, a, p, x, w_router, dx_add, dx, dz, expert, part);
+                                                                                  expert, split, alive);
+        const bool even = a.H % 2 == 0;
+        const auto run = a.bf16 ? (even ? &route_backward_typed<true, true> : &route_backward_typed<true, false>)
+                                : (even ? &route_backward_typed<false, true> : &route_backward_typed<false, false>);
+        run(st, a, p, x, w_router, dx_add, dx, dz, expert, reinterpret_cast<const u32x2*>(split), alive, part);
     }
     const int64_t slice = (static_cast<int64_t>(a.H) + 1) * a.E;
     route_dw_sum<<<static_cast<unsigned>((slice + 255) / 256), 256, 0, st>>>(

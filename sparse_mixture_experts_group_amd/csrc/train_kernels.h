@@ -62,7 +62,7 @@ struct RouteBackwardArgs {
 
 struct RouteBackwardPlan {
     int splits;                  // token ranges whose partial dW_r are added up
-    size_t dz, expert, part, total;   // workspace offsets and size
+    size_t dz, expert, split, live, part, total;   // workspace offsets and size
 };
 RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K);
 void launch_route_backward(hipStream_t st, const RouteBackwardArgs& a, const RouteBackwardPlan& plan, const void* x,
