@@ -10,7 +10,7 @@ namespace beam {
 namespace {
 
 constexpr int kColTile = 128;      // hidden columns of a dx block
-constexpr int kDxStride = kColTile + 2;
+constexpr int kDxStride = kColTile + 4;       // 16-byte rows, neighbours four banks apart
 constexpr int kDwTokens = 32;      // tokens of one stage of a dW block
 constexpr int kDwAhead = 4;        // stages in flight (even: the buffers alternate)
 constexpr int kCUs = 256;
@@ -105,8 +105,6 @@ __global__ __launch_bounds__(256) void route_dz(RouteBackwardArgs a, int group, 
     if (here && i == 0) alive[t] = (any & ((1ull << group) - 1)) != 0;
 }
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
 // Row t of an activation array (t is the same for the whole wave: a scalar address).
 template <bool BF16>
 __device__ __forceinline__ const void* row_at(const void* base, int64_t t, int H) {
@@ -120,10 +118,6 @@ __device__ __forceinline__ const void* row_at(const void* base, int64_t t, int H
 template <bool BF16>
 struct Pair {
     uint32_t w[BF16 ? 1 : 2];
-    __device__ __forceinline__ f32x2 wide() const {
-        if constexpr (BF16) return f32x2{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u)};
-        else return f32x2{__uint_as_float(w[0]), __uint_as_float(w[1])};
-    }
 };
 
 template <bool BF16, bool EVEN>
@@ -153,36 +147,28 @@ __device__ __forceinline__ Pair<BF16> load2(const void* row, uint32_t H, uint32_
     return p;
 }
 
-template <bool BF16, bool EVEN>
-__device__ __forceinline__ void store2(void* row, uint32_t H, uint32_t c, f32x2 v) {
-    if constexpr (EVEN) {
-        if (c >= H) return;
-        if constexpr (BF16)
-            static_cast<uint32_t*>(row)[c / 2] = static_cast<uint32_t>(f32_to_bf16_bits(v[0])) |
-                                                 (static_cast<uint32_t>(f32_to_bf16_bits(v[1])) << 16);
-        else static_cast<f32x2*>(row)[c / 2] = v;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (c + k >= H) continue;
-            if constexpr (BF16) static_cast<uint16_t*>(row)[c + k] = f32_to_bf16_bits(v[k]);
-            else static_cast<float*>(row)[c + k] = v[k];
-        }
-    }
+// The value that lane N of this lane's row of 16 holds.
+template <int N>
+__device__ __forceinline__ uint32_t of_row_lane(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xf, 0xf, true);      // row_newbcast:N
 }
 
-__device__ __forceinline__ float lane_float(float v, int l) {
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
+// The value of the next lane of the row of 16 (the last lane: of the first).
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x12f, 0xf, 0xf, true);          // row_ror:15
 }
 
 // ---------------------------------------------------------------------------
 // dx[t] = dx_add[t] + sum_i dz_i W[:, e_i], FP32, one rounding.  A block holds 128 columns
 // of W for all experts in LDS (expert-major, 130 KB for 256 experts: one block a CU) and
-// walks its tokens, two columns a lane: K reads of 512 bytes a token instead of a dense
-// product over E.  A wave takes up to 8 tokens at a time (64 picks, a pick a lane); the
-// picks and addends of its next tokens are loaded before it works on these.
+// walks its tokens: K reads of 512 bytes a token instead of a dense product over E.  A row
+// of 16 lanes takes a token, 8 columns a lane, and holds the token's picks, a pick a lane
+// (two for K > 16), which its lanes take from each other inside the vector instructions.
+// The picks and addends of a wave's next tokens are loaded before it works on these.
 // ---------------------------------------------------------------------------
-template <bool BF16, bool EVEN, int KT, bool ADD>
+constexpr int kDxStep = 2;         // tokens of a row of lanes in flight
+
+template <bool BF16, bool ALIGNED, int KT, bool ADD>
 __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t per_split, const float* __restrict__ wr,
                                                  const float* __restrict__ dz, const int32_t* __restrict__ expert,
                                                  const void* dx_add, void* dx) {
@@ -201,59 +187,79 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
         }
     }
     __syncthreads();
+    static_assert(KT <= 16, "one pick a lane");
+    constexpr int NP = KT > 0 ? 1 : 2;                 // picks a lane
     const int K = KT > 0 ? KT : a.K;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, in_row = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int batch = KT > 0 ? 8 : (K <= 8 ? 8 : 64 / K);       // tokens a wave takes at a time
     const int64_t t0 = per_split * blockIdx.y;
     const int64_t t1 = t0 + per_split < a.T ? t0 + per_split : a.T;
-    const int c = c0 + lane * 2;
-    const int64_t last = t1 * K - 1;
-    int e_next = -1;
-    float v_next = 0.0f;
-    Pair<BF16> add_next[8];
-    f32x2 add[8];
-    auto fetch = [&](int64_t t) {
-        const int64_t p = t * K + lane < last ? t * K + lane : last;
-        e_next = expert[p];
-        v_next = dz[p];
-        if constexpr (ADD) {
+    const int c = c0 + in_row * 8, n = a.H - c;
+    const f32x4* mine = reinterpret_cast<const f32x4*>(s_w) + in_row * 2;
+    int e[kDxStep][NP], e_next[kDxStep][NP];
+    float v[kDxStep][NP], v_next[kDxStep][NP];
+    Raw8<BF16> add[kDxStep], add_next[kDxStep];
+    auto fetch = [&](int64_t t) {                      // t: the wave's first token
 #pragma unroll
-            for (int j = 0; j < 8; ++j) add_next[j] = load2<BF16, EVEN>(row_at<BF16>(dx_add, t + j < t1 ? t + j : t1 - 1, a.H), a.H, c);
+        for (int s = 0; s < kDxStep; ++s) {
+            const int64_t mt = t + s * 4 + (lane >> 4), at = mt < t1 ? mt : t1 - 1;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const int i = in_row + 16 * q;
+                e_next[s][q] = expert[at * K + (i < K ? i : 0)];
+                v_next[s][q] = dz[at * K + (i < K ? i : 0)];
+            }
+            if constexpr (ADD) {
+                if (n > 0) add_next[s] = load_raw8<BF16, ALIGNED>(dx_add, at * a.H + c, n);
+            }
         }
     };
-    int64_t t = t0 + static_cast<int64_t>(wave) * batch;
+    constexpr int kStride = 16 * 4 * kDxStep;          // tokens of the block's sixteen waves
+    int64_t t = t0 + wave * 4 * kDxStep;
     if (t < t1) fetch(t);
-    for (; t < t1; t += 16 * batch) {
-        // no pick: expert 0 with factor 0 (the router's weights are finite)
-        const int at = (e_next > 0 ? e_next : 0) * (kDxStride / 2);
-        const float v = e_next >= 0 ? v_next : 0.0f;
+    for (; t < t1; t += kStride) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) add[j] = ADD ? add_next[j].wide() : f32x2{0.0f, 0.0f};
-        if (t + 16 * batch < t1) fetch(t + 16 * batch);
-        const f32x2* mine = reinterpret_cast<const f32x2*>(s_w) + lane;
-        auto pick = [&](int l, f32x2& acc) {
-            const float f = lane_float(v, l);
-            const f32x2 w = mine[__builtin_amdgcn_readlane(at, l)];
-            acc[0] = fmaf(f, w[0], acc[0]);
-            acc[1] = fmaf(f, w[1], acc[1]);
-        };
-        const int m = t1 - t < batch ? static_cast<int>(t1 - t) : batch;
-        if (KT > 0 && m == 8) {
+        for (int s = 0; s < kDxStep; ++s) {
+            add[s] = add_next[s];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int i = 0; i < KT; ++i) pick(j * KT + i, add[j]);
-                store2<BF16, EVEN>(const_cast<void*>(row_at<BF16>(dx, t + j, a.H)), a.H, c, add[j]);
+            for (int q = 0; q < NP; ++q) {
+                // no pick: expert 0 with factor 0 (the router's weights are finite)
+                e[s][q] = (e_next[s][q] > 0 ? e_next[s][q] : 0) * (kDxStride / 4);
+                v[s][q] = e_next[s][q] >= 0 ? v_next[s][q] : 0.0f;
             }
-        } else {
+        }
+        if (t + kStride < t1) fetch(t + kStride);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j < m) {
-                    for (int i = 0; i < K; ++i) pick(j * K + i, add[j]);
-                    store2<BF16, EVEN>(const_cast<void*>(row_at<BF16>(dx, t + j, a.H)), a.H, c, add[j]);
+        for (int s = 0; s < kDxStep; ++s) {
+            float acc[8] = {};
+            if constexpr (ADD) widen8<BF16>(add[s], acc);
+            auto pick = [&](uint32_t at, uint32_t factor) {
+                const float f = __uint_as_float(factor);
+                const f32x4 a0 = mine[at], a1 = mine[at + 1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[k] = fmaf(f, a0[k], acc[k]);
+                    acc[4 + k] = fmaf(f, a1[k], acc[4 + k]);
+                }
+            };
+            if constexpr (KT > 0) {
+                static_for<0, KT>([&](auto i) {
+                    pick(of_row_lane<i>(e[s][0]), of_row_lane<i>(__float_as_uint(v[s][0])));
+                });
+            } else {
+                uint32_t er = e[s][0], vr = __float_as_uint(v[s][0]);
+                for (int i = 0; i < K; ++i) {          // lane 0's pick, then the row moves up by one
+                    if (i == 16) {
+                        er = e[s][NP - 1];
+                        vr = __float_as_uint(v[s][NP - 1]);
+                    }
+                    pick(of_row_lane<0>(er), of_row_lane<0>(vr));
+                    er = row_rotate(er);
+                    vr = row_rotate(vr);
                 }
             }
+            const int64_t mt = t + s * 4 + (lane >> 4);
+            if (mt < t1 && n > 0) store_raw8<BF16, ALIGNED>(dx, mt * a.H + c, n, narrow8<BF16>(acc));
         }
     }
 }
@@ -491,13 +497,13 @@ __global__ __launch_bounds__(256) void route_dw_sum(int64_t n, int64_t slice, in
     else if (dbias) dbias[i - bias_at] = v;
 }
 
-template <bool BF16, bool EVEN, int KT>
+template <bool BF16, bool ALIGNED, int KT>
 static void dx_launch(hipStream_t st, const RouteBackwardArgs& a, const float* w_router, const float* dz,
                       const int32_t* expert, const void* dx_add, void* dx) {
     const int tiles = (a.H + kColTile - 1) / kColTile;
     const int splits = token_splits(a.T, tiles, 64);
     const int64_t per = (a.T + splits - 1) / splits;
-    const auto kernel = dx_add ? &route_dx<BF16, EVEN, KT, true> : &route_dx<BF16, EVEN, KT, false>;
+    const auto kernel = dx_add ? &route_dx<BF16, ALIGNED, KT, true> : &route_dx<BF16, ALIGNED, KT, false>;
     lds_opt_in(reinterpret_cast<const void*>(kernel), sizeof(float) * kMaxExperts * kDxStride);
     kernel<<<dim3(tiles, splits), 1024, sizeof(float) * a.E * kDxStride, st>>>(a, per, w_router, dz, expert, dx_add, dx);
 }
@@ -517,8 +523,10 @@ static void route_backward_typed(hipStream_t st, const RouteBackwardArgs& a, con
                                  const float* w_router, const void* dx_add, void* dx, const float* dz,
                                  const int32_t* expert, const u32x2* split, const uint8_t* alive, float* part) {
     if (dx) {
-        if (a.K == 8) dx_launch<BF16, EVEN, 8>(st, a, w_router, dz, expert, dx_add, dx);
-        else dx_launch<BF16, EVEN, 0>(st, a, w_router, dz, expert, dx_add, dx);
+        const bool al = a.H % 8 == 0;
+        if (al && a.K == 8) dx_launch<BF16, true, 8>(st, a, w_router, dz, expert, dx_add, dx);
+        else if (al) dx_launch<BF16, true, 0>(st, a, w_router, dz, expert, dx_add, dx);
+        else dx_launch<BF16, false, 0>(st, a, w_router, dz, expert, dx_add, dx);
     }
     const int me = dw_experts(a.E);
     if (me == 64) dw_launch<BF16, EVEN, 64>(st, a, p.splits, x, split, alive, part);
