@@ -12,19 +12,18 @@ namespace {
 constexpr int kColTile = 128;      // hidden columns of a dx block
 constexpr int kDxStride = kColTile + 4;       // 16-byte rows, neighbours four banks apart
 constexpr int kDwTokens = 32;      // tokens of one stage of a dW block
-constexpr int kDwAhead = 4;        // stages in flight (even: the buffers alternate)
+constexpr int kDwCols = 128;       // its hidden columns
 constexpr int kCUs = 256;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Experts (padded) and hidden columns of a dW block.
+// Experts of a dW block.
 int dw_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
-int dw_cols(int E) { return E <= 64 ? 256 : 128; }
 
-// Ranges that T tokens are cut into so that `tiles` blocks a range fill the chip, a range
-// no shorter than `least` tokens.
-int token_splits(int64_t T, int64_t tiles, int least) {
-    int64_t s = kCUs / tiles;
+// Ranges that T tokens are cut into so that `tiles` blocks a range give a CU `blocks` of
+// them, a range no shorter than `least` tokens.
+int token_splits(int64_t T, int64_t tiles, int blocks, int least) {
+    int64_t s = blocks * kCUs / tiles;
     if (s > (T + least - 1) / least) s = (T + least - 1) / least;
     return static_cast<int>(s < 1 ? 1 : s);
 }
@@ -33,15 +32,14 @@ int token_splits(int64_t T, int64_t tiles, int least) {
 
 RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K) {
     RouteBackwardPlan p;
-    const int nt = dw_cols(E);
-    const int64_t tiles = (static_cast<int64_t>(H) + 1 + nt - 1) / nt;       // a column for the bias
-    p.splits = T == 0 ? 0 : token_splits(T, tiles, 2 * kDwTokens);
+    const int64_t tiles = (static_cast<int64_t>(H) + kDwCols) / kDwCols;     // a column for the bias
+    p.splits = T == 0 ? 0 : token_splits(T, tiles, 2, 2 * kDwTokens);
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += align256(bytes); return o; };
     p.dz = take(sizeof(float) * T * K);
     p.expert = take(sizeof(int32_t) * T * K);
     p.split = take(8 * T * K);
-    p.live = take(T + 4);                      // read four at a time
+    p.live = take(T + 8);                      // read eight at a time
     p.part = take(sizeof(float) * p.splits * (static_cast<size_t>(H) + 1) * E);
     p.total = off;
     return p;
@@ -271,157 +269,153 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
 // three operands, and x is one (BF16) or three (FP32, where the six products of largest
 // order are kept: the others are under 2^-24 of the result's terms).  Sums in FP32.
 //
-// A block: ME experts x NT columns, eight waves of 64 experts x NW columns (32 x 32 x 16
-// products).  A stage of 32 tokens lies in LDS as rows of 64 bytes (one expert or column,
-// 32 tokens): x is transposed in registers on its way in, dz is scattered (at most K
-// entries a token) into rows that hold zeros, and its entries are taken out again before
-// the buffer's next stage.  Two buffers: a stage's loads are in flight during the products
-// of the stage before it.  Token ranges (blockIdx.y) write partial sums [H+1, E].
-// ---------------------------------------------------------------------------
-template <bool BF16, int ME>
+// A block: ME experts x 128 columns, four waves of 64 experts x NW columns (32 x 32 x 16
+// products).  A stage of 32 tokens lies in LDS as rows of 64 bytes (one expert's operand or
+// one column, 32 tokens): x is transposed in registers on its way in, dz is scattered (at
+// most K entries a token) into rows that hold zeros, and its entries are taken out again
+// after the products.  One buffer: two blocks share a CU (57 KB each for 256 experts and
+// BF16), and one's products run while the other writes its stage.  A stage's values are
+// loaded into registers a stage ahead.  Token ranges (blockIdx.y) write partial sums
+// [H+1, E].
+template <bool BF16, int ME, int Q_>
 struct DwTile {
-    static constexpr int WM = ME / 64, WN = 8 / WM;
-    static constexpr int NW = ME == 256 ? 64 : 32, NT = WN * NW, TN = NW / 32;
+    static constexpr int W = 4, kThreads = W * 64;       // waves, threads
+    static constexpr int WM = ME / 64, WN = W / WM;
+    static constexpr int NW = kDwCols / WN, TN = NW / 32;
     static constexpr int XS = BF16 ? 1 : 3;
-    static constexpr int kRows = 3 * ME + XS * NT;       // LDS rows of a stage
-    static constexpr int kLds = 2 * kRows * kStageRowBytes;
+    static constexpr int TPW = kDwTokens / W;            // tokens whose columns a wave brings in
+    static constexpr int Q = Q_;                         // picks a thread (32 K over 256 threads)
+    static constexpr int kX = 3 * (ME + 1) * kStageRowBytes;         // the columns' rows
+    static constexpr int kLds = kX + XS * kDwCols * kStageRowBytes;
+    static_assert(TPW == 8 && kDwCols == 128, "a column's eight tokens are one 16-byte chunk, two columns a lane");
+    static_assert(kLds <= 80 * 1024, "two blocks a CU");
 };
 
-template <bool BF16, bool EVEN, int ME>
-__global__ __launch_bounds__(512) void route_dw(RouteBackwardArgs a, int64_t per_split, const void* __restrict__ x,
-                                                const u32x2* __restrict__ split, const uint8_t* __restrict__ alive,
-                                                float* __restrict__ part) {
-    using L = DwTile<BF16, ME>;
+// Byte of operand k of expert e, 16-byte chunk (8 tokens) `chunk`: the operands of an expert
+// are neighbours; 16 experts' chunks of one product cover all banks.
+__device__ __forceinline__ int dz_offset(int e, int k, int chunk) {
+    return (e * 3 + k) * kStageRowBytes + ((chunk ^ ((e >> 2) & 3)) << 4);
+}
+
+template <bool BF16, bool EVEN, int ME, int Q_>
+__global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t per_split, const void* __restrict__ x,
+                                                   const u32x2* __restrict__ split, const uint8_t* __restrict__ alive,
+                                                   float* __restrict__ part) {
+    using L = DwTile<BF16, ME, Q_>;
     extern __shared__ __attribute__((aligned(16))) char s_stage[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % L::WM, wn = wave / L::WM;
-    const int c0 = blockIdx.x * L::NT;
-    const bool edge = c0 + L::NT > a.H;        // the tile holds the bias' column
+    const int c0 = blockIdx.x * kDwCols, col = lane * 2;
     const int64_t t0 = per_split * blockIdx.y;
     const int64_t t1 = t0 + per_split < a.T ? t0 + per_split : a.T;
-    for (int j = tid; j < L::kLds / 16; j += 512) reinterpret_cast<u32x4*>(s_stage)[j] = u32x4{0, 0, 0, 0};
+    for (int j = tid; j < L::kLds / 16; j += L::kThreads) reinterpret_cast<u32x4*>(s_stage)[j] = u32x4{0, 0, 0, 0};
 
-    constexpr int NP = L::NT / 128;            // column pairs of a lane
     struct Stage {
-        Pair<BF16> x[NP][4];                   // a lane's columns of its wave's four tokens
-        uint32_t live;                         // a byte each
-        u32x2 pick[2];                         // a thread's picks
-    } ahead[kDwAhead];
-    // thread -> up to two of the stage's 32 K picks, and the token's place in an LDS row
-    const int picks = kDwTokens * a.K;
-    const bool two = picks > 512;
-    int chunk[2], byte[2], old[2][2] = {{-1, -1}, {-1, -1}};     // old: LDS places per buffer
+        Pair<BF16> x[L::TPW];                  // a lane's two columns of its wave's tokens
+        u32x2 live;                            // a byte each
+        u32x2 pick[L::Q];                      // a thread's picks
+    } ahead[2];
+    Pair<BF16> ones;                           // 1 in the bias' column
+    if constexpr (BF16) {
+        ones.w[0] = c0 + col == a.H ? 0x3F80u : c0 + col + 1 == a.H ? 0x3F800000u : 0u;
+    } else {
+        ones.w[0] = c0 + col == a.H ? 0x3F800000u : 0u;
+        ones.w[1] = c0 + col + 1 == a.H ? 0x3F800000u : 0u;
+    }
+    // thread -> its picks among the stage's 32 K, and their token's place in an LDS row
+    int chunk[L::Q], byte[L::Q], old[L::Q];    // old: where its picks lie in LDS
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int tok = (tid + 512 * q) / a.K;
+    for (int q = 0; q < L::Q; ++q) {
+        const int i = tid + L::kThreads * q, tok = i < kDwTokens * a.K ? i / a.K : 0;
         chunk[q] = tok >> 3;
         byte[q] = (tok & 7) * 2;
     }
-    const int64_t last = t1 * a.K - 1;
+    const int64_t end = t1 * a.K;
     auto fetch = [&](Stage& f, int64_t t) {
-        const int64_t tw = t + wave * 4;
-        f.live = *reinterpret_cast<const uint32_t*>(alive + (tw < t1 ? tw : t0));   // tw is a multiple of 4
+        const int64_t tw = t + wave * L::TPW;                    // a multiple of 8
+        f.live = *reinterpret_cast<const u32x2*>(alive + (tw < t1 ? tw : t0));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const void* row = row_at<BF16>(x, tw + j < t1 ? tw + j : t1 - 1, a.H);
+        for (int j = 0; j < L::TPW; ++j)
+            f.x[j] = load2<BF16, EVEN>(row_at<BF16>(x, tw + j < t1 ? tw + j : t1 - 1, a.H), a.H, c0 + col);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) f.x[q][j] = load2<BF16, EVEN>(row, a.H, c0 + q * 128 + lane * 2);
-        }
-        const int64_t p0 = t * a.K + tid;
-        f.pick[0] = split[p0 < last ? p0 : last];
-        if (two) f.pick[1] = split[p0 + 512 < last ? p0 + 512 : last];
-    };
-    auto clear = [&](int b) {
-        char* s = s_stage + b * L::kRows * kStageRowBytes;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if ((q == 0 || two) && old[b][q] >= 0) {
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint16_t*>(s + k * ME * kStageRowBytes + old[b][q]) = 0;
-            }
+        for (int q = 0; q < L::Q; ++q) {
+            const int64_t p = t * a.K + tid + L::kThreads * q;
+            f.pick[q] = split[p < end ? p : end - 1];
         }
     };
-    auto fill_dz = [&](int b, const Stage& f, int64_t t) {
-        char* s = s_stage + b * L::kRows * kStageRowBytes;
+    auto clear = [&]() {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (q == 1 && !two) continue;
-            const int i = tid + 512 * q, e = f.pick[q][1] >> 16;
-            old[b][q] = -1;
-            if (i < picks && t * a.K + i <= last && e != 0xFFFF) {
-                old[b][q] = stage_offset(e, chunk[q]) + byte[q];
-                *reinterpret_cast<uint16_t*>(s + old[b][q]) = static_cast<uint16_t>(f.pick[q][0]);
-                *reinterpret_cast<uint16_t*>(s + ME * kStageRowBytes + old[b][q]) =
-                    static_cast<uint16_t>(f.pick[q][0] >> 16);
-                *reinterpret_cast<uint16_t*>(s + 2 * ME * kStageRowBytes + old[b][q]) =
-                    static_cast<uint16_t>(f.pick[q][1]);
-            }
+        for (int q = 0; q < L::Q; ++q)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint16_t*>(s_stage + old[q] + k * kStageRowBytes) = 0;
+    };
+    auto fill_dz = [&](const Stage& f, int64_t t) {
+#pragma unroll
+        for (int q = 0; q < L::Q; ++q) {
+            const int i = tid + L::kThreads * q, e = f.pick[q][1] >> 16;
+            const bool is = i < kDwTokens * a.K && t * a.K + i < end && e != 0xFFFF;
+            old[q] = dz_offset(is ? e : ME, 0, chunk[q]) + byte[q];          // none: a row of its own
+            uint16_t* to = reinterpret_cast<uint16_t*>(s_stage + old[q]);
+            to[0] = static_cast<uint16_t>(f.pick[q][0]);
+            to[kStageRowBytes / 2] = static_cast<uint16_t>(f.pick[q][0] >> 16);
+            to[kStageRowBytes] = static_cast<uint16_t>(f.pick[q][1]);
         }
     };
-    auto fill_x = [&](int b, const Stage& f, int64_t t) {
-        char* sx = s_stage + (b * L::kRows + 3 * ME) * kStageRowBytes;
+    auto fill_x = [&](const Stage& f, int64_t t) {
+        Pair<BF16> v[L::TPW];
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const int col = q * 128 + lane * 2;
-            Pair<BF16> v[4];
+        for (int j = 0; j < L::TPW; ++j) {
+            // a token without picks is not looked at (live holds 0 or 1 a byte)
+            const uint32_t in = t + wave * L::TPW + j < t1 ? 1 : 0;
+            const uint32_t mask = 0u - ((f.live[j >> 2] >> (8 * (j & 3))) & in);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // a token without picks is not looked at
-                const bool in = ((f.live >> (8 * j)) & 0xff) && t + wave * 4 + j < t1;
+            for (int k = 0; k < (BF16 ? 1 : 2); ++k) v[j].w[k] = (f.x[j].w[k] & mask) | ones.w[k];
+        }
 #pragma unroll
-                for (int k = 0; k < (BF16 ? 1 : 2); ++k) v[j].w[k] = in ? f.x[q][j].w[k] : 0;
-                if (edge) {                    // the bias' column is ones
-                    if constexpr (BF16) {
-                        v[j].w[0] |= c0 + col == a.H ? 0x3F80u : c0 + col + 1 == a.H ? 0x3F800000u : 0u;
-                    } else {
-                        v[j].w[0] |= c0 + col == a.H ? 0x3F800000u : 0u;
-                        v[j].w[1] |= c0 + col + 1 == a.H ? 0x3F800000u : 0u;
-                    }
-                }
-            }
+        for (int k = 0; k < 2; ++k) {          // a column: the wave's eight tokens, a chunk
+            char* to = s_stage + L::kX + stage_offset(col + k, wave);
+            if constexpr (BF16) {
+                const uint32_t sel = k == 0 ? 0x05040100u : 0x07060302u;          // low or high halves
+                u32x4 o;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {      // a column: four tokens, 8 bytes
-                char* to = sx + stage_offset(col + k, wave >> 1) + (wave & 1) * 8;
-                if constexpr (BF16) {
-                    const uint32_t sel = k == 0 ? 0x05040100u : 0x07060302u;      // low or high halves
-                    *reinterpret_cast<u32x2*>(to) = u32x2{__builtin_amdgcn_perm(v[1].w[0], v[0].w[0], sel),
-                                                          __builtin_amdgcn_perm(v[3].w[0], v[2].w[0], sel)};
-                } else {
-                    uint16_t p[4][3];
+                for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(v[2 * j + 1].w[0], v[2 * j].w[0], sel);
+                *reinterpret_cast<u32x4*>(to) = o;
+            } else {
+                uint16_t p[L::TPW][3];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) split3(__uint_as_float(v[j].w[k]), p[j]);
+                for (int j = 0; j < L::TPW; ++j) split3(__uint_as_float(v[j].w[k]), p[j]);
 #pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        *reinterpret_cast<u32x2*>(to + m * L::NT * kStageRowBytes) =
-                            u32x2{p[0][m] | (static_cast<uint32_t>(p[1][m]) << 16),
-                                  p[2][m] | (static_cast<uint32_t>(p[3][m]) << 16)};
+                for (int m = 0; m < 3; ++m) {
+                    u32x4 o;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = p[2 * j][m] | (static_cast<uint32_t>(p[2 * j + 1][m]) << 16);
+                    *reinterpret_cast<u32x4*>(to + m * kDwCols * kStageRowBytes) = o;
                 }
             }
         }
     };
 
     f32x16 acc[2][L::TN] = {};
-    auto products = [&](int b) {
-        const char* s = s_stage + b * L::kRows * kStageRowBytes;
-        const char* sx = s + 3 * ME * kStageRowBytes;
+    auto products = [&]() {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            const int chunk = ks * 2 + (lane >> 5);
+            const int ch = ks * 2 + (lane >> 5);
             bf16x8 fz[2][3], fx[L::TN][L::XS];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
-                    fz[i][k] = *reinterpret_cast<const bf16x8*>(
-                        s + k * ME * kStageRowBytes + stage_offset(wm * 64 + i * 32 + (lane & 31), chunk));
+                    fz[i][k] = *reinterpret_cast<const bf16x8*>(s_stage +
+                                                                dz_offset(wm * 64 + i * 32 + (lane & 31), k, ch));
 #pragma unroll
             for (int i = 0; i < L::TN; ++i)
 #pragma unroll
                 for (int k = 0; k < L::XS; ++k)
                     fx[i][k] = *reinterpret_cast<const bf16x8*>(
-                        sx + k * L::NT * kStageRowBytes + stage_offset(wn * L::NW + i * 32 + (lane & 31), chunk));
+                        s_stage + L::kX + k * kDwCols * kStageRowBytes +
+                        stage_offset(wn * L::NW + i * 32 + (lane & 31), ch));
 #pragma unroll
             for (int order = 2; order >= 0; --order)     // small products first
 #pragma unroll
@@ -439,26 +433,23 @@ __global__ __launch_bounds__(512) void route_dw(RouteBackwardArgs a, int64_t per
 
     __syncthreads();
     if (t0 < t1) {
-        static_for<0, kDwAhead>([&](auto u) { fetch(ahead[u], t0 + u * kDwTokens); });
-        fill_x(0, ahead[0], t0);
-        fill_dz(0, ahead[0], t0);
+        fetch(ahead[0], t0);
+        fetch(ahead[1], t0 + kDwTokens);
+        fill_x(ahead[0], t0);
+        fill_dz(ahead[0], t0);
     }
-    __syncthreads();
-    for (int64_t t = t0; t < t1; t += kDwAhead * kDwTokens) {
-        static_for<0, kDwAhead>([&](auto u) {
-            constexpr int b = u & 1, next = (u + 1) % kDwAhead;
+    // pairs of stages, the last one perhaps empty
+    for (int64_t t = t0; t < t1; t += 2 * kDwTokens) {
+        static_for<0, 2>([&](auto u) {
             const int64_t tu = t + u * kDwTokens;
-            if (tu >= t1) return;
-            const bool more = tu + kDwTokens < t1;
-            fetch(ahead[u], tu + kDwAhead * kDwTokens);          // its values lie in the buffer
-            // the other buffer's products are done (the barriers below): its entries go, and
-            // its columns come
-            clear(b ^ 1);
-            if (more) fill_x(b ^ 1, ahead[next], tu + kDwTokens);
-            products(b);
-            lds_pipeline_barrier();            // every entry is out before a new one goes in
-            if (more) fill_dz(b ^ 1, ahead[next], tu + kDwTokens);
-            lds_pipeline_barrier();
+            lds_pipeline_barrier();            // the stage is written
+            fetch(ahead[u], tu + 2 * kDwTokens);
+            products();
+            lds_pipeline_barrier();            // and read
+            clear();
+            fill_x(ahead[u ^ 1], tu + kDwTokens);
+            lds_pipeline_barrier();            // no entry of it is left
+            fill_dz(ahead[u ^ 1], tu + kDwTokens);
         });
     }
 
@@ -501,21 +492,28 @@ template <bool BF16, bool ALIGNED, int KT>
 static void dx_launch(hipStream_t st, const RouteBackwardArgs& a, const float* w_router, const float* dz,
                       const int32_t* expert, const void* dx_add, void* dx) {
     const int tiles = (a.H + kColTile - 1) / kColTile;
-    const int splits = token_splits(a.T, tiles, 64);
+    const int splits = token_splits(a.T, tiles, 1, 64);
     const int64_t per = (a.T + splits - 1) / splits;
     const auto kernel = dx_add ? &route_dx<BF16, ALIGNED, KT, true> : &route_dx<BF16, ALIGNED, KT, false>;
     lds_opt_in(reinterpret_cast<const void*>(kernel), sizeof(float) * kMaxExperts * kDxStride);
     kernel<<<dim3(tiles, splits), 1024, sizeof(float) * a.E * kDxStride, st>>>(a, per, w_router, dz, expert, dx_add, dx);
 }
 
+template <bool BF16, bool EVEN, int ME, int Q>
+static void dw_launch_picks(hipStream_t st, const RouteBackwardArgs& a, int splits, const void* x, const u32x2* split,
+                            const uint8_t* alive, float* part) {
+    using L = DwTile<BF16, ME, Q>;
+    const int64_t per = ((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens;
+    lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16, EVEN, ME, Q>), L::kLds);
+    route_dw<BF16, EVEN, ME, Q><<<dim3((a.H + kDwCols) / kDwCols, splits), L::kThreads, L::kLds, st>>>(
+        a, per, x, split, alive, part);
+}
+
 template <bool BF16, bool EVEN, int ME>
 static void dw_launch(hipStream_t st, const RouteBackwardArgs& a, int splits, const void* x, const u32x2* split,
                       const uint8_t* alive, float* part) {
-    using L = DwTile<BF16, ME>;
-    const int64_t per = ((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens;
-    lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16, EVEN, ME>), L::kLds);
-    route_dw<BF16, EVEN, ME><<<dim3((a.H + 1 + L::NT - 1) / L::NT, splits), 512, L::kLds, st>>>(a, per, x, split,
-                                                                                               alive, part);
+    if (a.K <= 8) dw_launch_picks<BF16, EVEN, ME, 1>(st, a, splits, x, split, alive, part);
+    else dw_launch_picks<BF16, EVEN, ME, 4>(st, a, splits, x, split, alive, part);
 }
 
 template <bool BF16, bool EVEN>
