@@ -334,61 +334,62 @@ def keep_blocks(cols: int) -> int:
 
 def _act_torch(cfg):
     import torch
-    t = {BEAM_DTYPE_F32: torch.float32, BEAM_DTYPE_BF16: torch.bfloat16}.get(cfg.act_dtype)
-    if t is None:
-        raise BeamMoEError(BEAM_ERR_UNSUPPORTED, "act_dtype")
-    return t
+    if cfg.act_dtype == BEAM_DTYPE_BF16:
+        return torch.bfloat16
+    if cfg.act_dtype == BEAM_DTYPE_F32:
+        return torch.float32
+    raise BeamMoEError(BEAM_ERR_UNSUPPORTED, "act_dtype")
 
 
-def _arg(name, t, shape, *dtypes):
-    """Checks one tensor's dtype and shape and that it is dense; returns its address (None
-    for None; an empty tensor has none)."""
+# Where a training operator runs: on the device of its tensors (all on one GPU), on the
+# caller's stream or that device's current one.  _elsewhere names the stream to switch to
+# when that is not where the caller stands: the operator then calls itself inside it, so
+# that its device is current and its outputs and temporaries belong to its stream (a
+# temporary is not handed out again before the stream is done with it).  The calls of a
+# decode step cost as much on the host as on the GPU, hence the short paths.
+def _elsewhere(stream, t):
+    import torch
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensor must be on the GPU")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+        return None if dev == torch.cuda.current_device() and stream == torch.cuda.current_stream(dev) else stream
+    return None if dev == torch.cuda.current_device() else torch.cuda.current_stream(dev)
+
+
+def _handle(t):
+    """The raw current stream of t's device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _arg(name, t, dev, shape, dtype, other=None):
+    """Checks one tensor's device, dtype (`dtype` or `other`) and shape and that it is dense;
+    returns its address (None for None; an empty tensor has none)."""
     if t is None:
         return None
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)} of shape {tuple(shape)}, "
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on GPU {dev}, got one on {t.device}")
+    if (t.dtype != dtype and t.dtype != other) or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype}{f' or {other}' if other else ''} of shape {tuple(shape)}, "
                          f"got {t.dtype} of shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr() or None
 
 
-class _On:
-    """Where a training operator runs: the device of its tensors (all on one GPU), and the
-    caller's stream or that device's current one.  Inside the context the device is
-    current and tensors are allocated for that stream, so a temporary of this call is not
-    handed out again before the stream is done with it."""
-
-    def __init__(self, stream, *tensors):
-        import torch
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("tensor must be on the GPU")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-        self.device = dev
-        current = torch.cuda.current_stream(dev)
-        self.stream = current if stream is None else stream
-        self.handle = self.stream.cuda_stream
-        here = dev.index == torch.cuda.current_device()
-        self._enter = None if here and self.stream == current else torch.cuda.stream(self.stream)
-
-    def __enter__(self):
-        if self._enter is not None:
-            self._enter.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._enter is not None:
-            self._enter.__exit__(*exc)
-        return False
+def _temporary(ws, need, like):
+    """(workspace to keep alive, address, bytes): the caller's, or `need` bytes."""
+    import torch
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = like.new_empty(need, dtype=torch.uint8)
+    elif ws.get_device() != like.get_device() or not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous and on the GPU of the other tensors")
+    return ws, ws.data_ptr() or None, ws.numel() * ws.element_size()
 
 
 def _rows_by(t, name):
@@ -413,21 +414,24 @@ def beam_moe_sort(cfg, ids, expert_off=None, row_of_pair=None, pair_of_row=None,
     """Rows for the picks `ids` [T, K] int32, by expert: (expert_off [E+1], row_of_pair
     [T, K], pair_of_row [T*K]), all int32.  Ids outside [0, E) are dropped (row -1)."""
     import torch
-    i32 = torch.int32
-    T, K, E = _rows_by(ids, "ids"), cfg.topk, cfg.n_experts
-    with _On(stream, ids, expert_off, row_of_pair, pair_of_row, ws) as on:
-        p_ids = _arg("ids", ids, (T, K), i32)
-        expert_off = torch.empty(max(E + 1, 1), dtype=i32, device=on.device) if expert_off is None else expert_off
-        row_of_pair = torch.empty((T, K), dtype=i32, device=on.device) if row_of_pair is None else row_of_pair
-        pair_of_row = torch.empty(T * K, dtype=i32, device=on.device) if pair_of_row is None else pair_of_row
-        if ws is None:
-            need = beam_moe_sort_workspace_size(cfg, T)
-            ws = torch.empty(need, dtype=torch.uint8, device=on.device) if need else None
-        st = lib().beam_moe_sort(ctypes.byref(cfg), T, p_ids, _arg("expert_off", expert_off, (E + 1,), i32),
-                                 _arg("row_of_pair", row_of_pair, (T, K), i32),
-                                 _arg("pair_of_row", pair_of_row, (T * K,), i32),
-                                 None if ws is None else _ptr(ws),
-                                 0 if ws is None else ws.numel() * ws.element_size(), on.handle)
+    T, K, E, i32 = _rows_by(ids, "ids"), cfg.topk, cfg.n_experts, torch.int32
+    on = _elsewhere(stream, ids)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_sort(cfg, ids, expert_off, row_of_pair, pair_of_row, ws)
+    dev = ids.get_device()
+    p_ids = _arg("ids", ids, dev, (T, K), i32)
+    expert_off = ids.new_empty(E + 1) if expert_off is None else expert_off
+    row_of_pair = ids.new_empty((T, K)) if row_of_pair is None else row_of_pair
+    pair_of_row = ids.new_empty(T * K) if pair_of_row is None else pair_of_row
+    fn, c = lib().beam_moe_sort, ctypes.byref(cfg)
+    args = (p_ids, _arg("expert_off", expert_off, dev, (E + 1,), i32), _arg("row_of_pair", row_of_pair, dev, (T, K), i32),
+            _arg("pair_of_row", pair_of_row, dev, (T * K,), i32))
+    ws, p_ws, n_ws = _temporary(ws, 0, ids)
+    st = fn(c, T, *args, p_ws, n_ws, _handle(ids))
+    if st == BEAM_ERR_WORKSPACE and ws is None:            # past one block's pairs
+        ws, p_ws, n_ws = _temporary(None, beam_moe_sort_workspace_size(cfg, T), ids)
+        st = fn(c, T, *args, p_ws, n_ws, _handle(ids))
     _check(st, "beam_moe_sort")
     return expert_off, row_of_pair, pair_of_row
 
@@ -440,23 +444,28 @@ def beam_moe_dispatch(cfg, x, row_of_pair, xs=None, rows=None, x_scale=None, kee
     rows=0 makes the copy alone (xs is None).  row_of_pair None: row t for token t."""
     import torch
     T, K, H, act = _rows_by(x, "x"), cfg.topk, cfg.hidden, _act_torch(cfg)
+    on = _elsewhere(stream, x)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_dispatch(cfg, x, row_of_pair, xs, rows, x_scale, keep8, keep_q, keep_scale)
     u8, f8 = torch.uint8, torch.float8_e4m3fn
+    dev = x.get_device()
+    p_x = _arg("x", x, dev, (T, H), act) if x_scale is None else _arg("x", x, dev, (T, H), f8, u8)
     copy_alone = xs is None and rows == 0
-    with _On(stream, x, row_of_pair, xs, x_scale, keep_q, keep_scale) as on:
-        if xs is not None:
-            rows = _rows_by(xs, "xs")
-        rows = T * K if rows is None else int(rows)
-        p_x = _arg("x", x, (T, H), *((act,) if x_scale is None else (f8, u8)))
-        if xs is None and not copy_alone:
-            xs = torch.empty((rows, H), dtype=act, device=on.device)
-        if keep8 and keep_q is None:
-            keep_q = torch.empty((T, H), dtype=f8, device=on.device)
-        if keep8 and keep_scale is None:
-            keep_scale = torch.empty((T, keep_blocks(H)), dtype=u8, device=on.device)
-        st = lib().beam_moe_dispatch(ctypes.byref(cfg), T, p_x, _arg("x_scale", x_scale, (T, keep_blocks(H)), u8),
-                                     _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
-                                     _arg("xs", xs, (rows, H), act), _arg("keep_q", keep_q, (T, H), f8, u8),
-                                     _arg("keep_scale", keep_scale, (T, keep_blocks(H)), u8), on.handle)
+    if xs is not None:
+        rows = _rows_by(xs, "xs")
+    rows = T * K if rows is None else int(rows)
+    if xs is None and not copy_alone:
+        xs = x.new_empty((rows, H), dtype=act)
+    nb = keep_blocks(H)
+    if keep8 and keep_q is None:
+        keep_q = x.new_empty((T, H), dtype=f8)
+    if keep8 and keep_scale is None:
+        keep_scale = x.new_empty((T, nb), dtype=u8)
+    st = lib().beam_moe_dispatch(ctypes.byref(cfg), T, p_x, _arg("x_scale", x_scale, dev, (T, nb), u8),
+                                 _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                 _arg("xs", xs, dev, (rows, H), act), _arg("keep_q", keep_q, dev, (T, H), f8, u8),
+                                 _arg("keep_scale", keep_scale, dev, (T, nb), u8), _handle(x))
     _check(st, "beam_moe_dispatch")
     return xs if keep_q is None else (xs, keep_q, keep_scale)
 
@@ -464,12 +473,17 @@ def beam_moe_dispatch(cfg, x, row_of_pair, xs=None, rows=None, x_scale=None, kee
 def beam_moe_dispatch_backward(cfg, dxs, row_of_pair, dx=None, stream=None):
     """dx[t] = sum of the gradients dxs [rows, H] of token t's rows: returns dx [T, H]."""
     import torch
-    rows, T, K, H, act = _rows_by(dxs, "dxs"), _rows_by(row_of_pair, "row_of_pair"), cfg.topk, cfg.hidden, _act_torch(cfg)
-    with _On(stream, dxs, row_of_pair, dx) as on:
-        dx = torch.empty((T, H), dtype=act, device=on.device) if dx is None else dx
-        st = lib().beam_moe_dispatch_backward(ctypes.byref(cfg), T, _arg("dxs", dxs, (rows, H), act),
-                                              _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
-                                              _arg("dx", dx, (T, H), act), on.handle)
+    rows, T, K, H = _rows_by(dxs, "dxs"), _rows_by(row_of_pair, "row_of_pair"), cfg.topk, cfg.hidden
+    act = _act_torch(cfg)
+    on = _elsewhere(stream, dxs)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_dispatch_backward(cfg, dxs, row_of_pair, dx)
+    dev = dxs.get_device()
+    dx = dxs.new_empty((T, H)) if dx is None else dx
+    st = lib().beam_moe_dispatch_backward(ctypes.byref(cfg), T, _arg("dxs", dxs, dev, (rows, H), act),
+                                          _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                          _arg("dx", dx, dev, (T, H), act), _handle(dxs))
     _check(st, "beam_moe_dispatch_backward")
     return dx
 
@@ -477,14 +491,18 @@ def beam_moe_dispatch_backward(cfg, dxs, row_of_pair, dx=None, stream=None):
 def beam_moe_combine(cfg, expert_out, row_of_pair, weights, y=None, stream=None):
     """y[t] = sum_i weights[t, i] * expert_out[row_of_pair[t, i]]: returns y [T, H]."""
     import torch
-    rows, T, K, H, act = (_rows_by(expert_out, "expert_out"), _rows_by(row_of_pair, "row_of_pair"), cfg.topk, cfg.hidden,
-                          _act_torch(cfg))
-    with _On(stream, expert_out, row_of_pair, weights, y) as on:
-        y = torch.empty((T, H), dtype=act, device=on.device) if y is None else y
-        st = lib().beam_moe_combine(ctypes.byref(cfg), T, _arg("expert_out", expert_out, (rows, H), act),
-                                    _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
-                                    _arg("weights", weights, (T, K), torch.float32), _arg("y", y, (T, H), act),
-                                    on.handle)
+    rows, T, K, H = _rows_by(expert_out, "expert_out"), _rows_by(row_of_pair, "row_of_pair"), cfg.topk, cfg.hidden
+    act = _act_torch(cfg)
+    on = _elsewhere(stream, expert_out)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_combine(cfg, expert_out, row_of_pair, weights, y)
+    dev = expert_out.get_device()
+    y = expert_out.new_empty((T, H)) if y is None else y
+    st = lib().beam_moe_combine(ctypes.byref(cfg), T, _arg("expert_out", expert_out, dev, (rows, H), act),
+                                _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                _arg("weights", weights, dev, (T, K), torch.float32), _arg("y", y, dev, (T, H), act),
+                                _handle(expert_out))
     _check(st, "beam_moe_combine")
     return y
 
@@ -495,22 +513,26 @@ def beam_moe_combine_backward(cfg, dy, expert_out, row_of_pair, weights, deo=Non
     with `rows` rows (T*K by default).  deo may be expert_out itself."""
     import torch
     T, K, H, act = _rows_by(dy, "dy"), cfg.topk, cfg.hidden, _act_torch(cfg)
-    with _On(stream, dy, expert_out, row_of_pair, weights, deo, dweights) as on:
-        for t in (deo, expert_out):
-            rows = _rows_by(t, "rows") if t is not None else rows
-        rows = T * K if rows is None else int(rows)
-        deo = torch.empty((rows, H), dtype=act, device=on.device) if deo is None else deo
-        if expert_out is not None and dweights is None:
-            dweights = torch.empty((T, K), dtype=torch.float32, device=on.device)
-        p_eo = _arg("expert_out", expert_out, (rows, H), act)
-        p_dw = _arg("dweights", dweights, (T, K), torch.float32)
-        if expert_out is not None and rows == 0:       # no row to read: every pair is dropped
-            dweights.zero_()
-            p_eo = p_dw = None
-        st = lib().beam_moe_combine_backward(ctypes.byref(cfg), T, _arg("dy", dy, (T, H), act), p_eo,
-                                             _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
-                                             _arg("weights", weights, (T, K), torch.float32),
-                                             _arg("deo", deo, (rows, H), act), p_dw, on.handle)
+    on = _elsewhere(stream, dy)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_combine_backward(cfg, dy, expert_out, row_of_pair, weights, deo, dweights, rows)
+    dev = dy.get_device()
+    for t in (deo, expert_out):
+        rows = _rows_by(t, "rows") if t is not None else rows
+    rows = T * K if rows is None else int(rows)
+    deo = dy.new_empty((rows, H)) if deo is None else deo
+    if expert_out is not None and dweights is None:
+        dweights = dy.new_empty((T, K), dtype=torch.float32)
+    p_eo = _arg("expert_out", expert_out, dev, (rows, H), act)
+    p_dw = _arg("dweights", dweights, dev, (T, K), torch.float32)
+    if expert_out is not None and rows == 0:               # no row to read: every pair is dropped
+        dweights.zero_()
+        p_eo = p_dw = None
+    st = lib().beam_moe_combine_backward(ctypes.byref(cfg), T, _arg("dy", dy, dev, (T, H), act), p_eo,
+                                         _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                         _arg("weights", weights, dev, (T, K), torch.float32),
+                                         _arg("deo", deo, dev, (rows, H), act), p_dw, _handle(dy))
     _check(st, "beam_moe_combine_backward")
     return deo, dweights
 
@@ -523,18 +545,22 @@ def beam_moe_swiglu(cfg, gu, weights=None, row_of_pair=None, h=None, keep8=False
     import torch
     rows, K, I, act = _rows_by(gu, "gu"), cfg.topk, cfg.inter, _act_torch(cfg)
     T = rows if row_of_pair is None else _rows_by(row_of_pair, "row_of_pair")
+    on = _elsewhere(stream, gu)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_swiglu(cfg, gu, weights, row_of_pair, h, keep8, keep_q, keep_scale)
     u8, f8 = torch.uint8, torch.float8_e4m3fn
-    with _On(stream, gu, weights, row_of_pair, h, keep_q, keep_scale) as on:
-        h = torch.empty((rows, I), dtype=act, device=on.device) if h is None else h
-        if keep8 and keep_q is None:
-            keep_q = torch.empty((rows, 2 * I), dtype=f8, device=on.device)
-        if keep8 and keep_scale is None:
-            keep_scale = torch.empty((rows, 2, keep_blocks(I)), dtype=u8, device=on.device)
-        st = lib().beam_moe_swiglu(ctypes.byref(cfg), T, _arg("gu", gu, (rows, 2 * I), act),
-                                   _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
-                                   _arg("weights", weights, (T, K), torch.float32), _arg("h", h, (rows, I), act),
-                                   _arg("keep_q", keep_q, (rows, 2 * I), f8, u8),
-                                   _arg("keep_scale", keep_scale, (rows, 2, keep_blocks(I)), u8), on.handle)
+    dev, nb = gu.get_device(), keep_blocks(I)
+    h = gu.new_empty((rows, I)) if h is None else h
+    if keep8 and keep_q is None:
+        keep_q = gu.new_empty((rows, 2 * I), dtype=f8)
+    if keep8 and keep_scale is None:
+        keep_scale = gu.new_empty((rows, 2, nb), dtype=u8)
+    st = lib().beam_moe_swiglu(ctypes.byref(cfg), T, _arg("gu", gu, dev, (rows, 2 * I), act),
+                               _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                               _arg("weights", weights, dev, (T, K), torch.float32), _arg("h", h, dev, (rows, I), act),
+                               _arg("keep_q", keep_q, dev, (rows, 2 * I), f8, u8),
+                               _arg("keep_scale", keep_scale, dev, (rows, 2, nb), u8), _handle(gu))
     _check(st, "beam_moe_swiglu")
     return h if keep_q is None else (h, keep_q, keep_scale)
 
@@ -547,20 +573,24 @@ def beam_moe_swiglu_backward(cfg, dh, gu, gu_scale=None, weights=None, row_of_pa
     import torch
     rows, K, I, act = _rows_by(gu, "gu"), cfg.topk, cfg.inter, _act_torch(cfg)
     T = rows if row_of_pair is None else _rows_by(row_of_pair, "row_of_pair")
-    u8, f8, f32 = torch.uint8, torch.float8_e4m3fn, torch.float32
-    with _On(stream, dh, gu, gu_scale, weights, row_of_pair, dgu, h, dweights) as on:
-        dgu = torch.empty((rows, 2 * I), dtype=act, device=on.device) if dgu is None else dgu
-        if again and h is None:
-            h = torch.empty((rows, I), dtype=act, device=on.device)
-        if weights is not None and dweights is None:
-            dweights = torch.empty((T, K), dtype=f32, device=on.device)
-        st = lib().beam_moe_swiglu_backward(ctypes.byref(cfg), T, _arg("dh", dh, (rows, I), act),
-                                            _arg("gu", gu, (rows, 2 * I), *((act,) if gu_scale is None else (f8, u8))),
-                                            _arg("gu_scale", gu_scale, (rows, 2, keep_blocks(I)), u8),
-                                            _arg("row_of_pair", row_of_pair, (T, K), torch.int32), rows,
-                                            _arg("weights", weights, (T, K), f32),
-                                            _arg("dgu", dgu, (rows, 2 * I), act), _arg("h", h, (rows, I), act),
-                                            _arg("dweights", dweights, (T, K), f32), on.handle)
+    on = _elsewhere(stream, dh)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_swiglu_backward(cfg, dh, gu, gu_scale, weights, row_of_pair, dgu, h, dweights, again)
+    u8, f32, dev = torch.uint8, torch.float32, dh.get_device()
+    dgu = dh.new_empty((rows, 2 * I)) if dgu is None else dgu
+    if again and h is None:
+        h = dh.new_empty((rows, I))
+    if weights is not None and dweights is None:
+        dweights = dh.new_empty((T, K), dtype=f32)
+    p_gu = _arg("gu", gu, dev, (rows, 2 * I), act) if gu_scale is None else \
+        _arg("gu", gu, dev, (rows, 2 * I), torch.float8_e4m3fn, u8)
+    st = lib().beam_moe_swiglu_backward(ctypes.byref(cfg), T, _arg("dh", dh, dev, (rows, I), act), p_gu,
+                                        _arg("gu_scale", gu_scale, dev, (rows, 2, keep_blocks(I)), u8),
+                                        _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                        _arg("weights", weights, dev, (T, K), f32),
+                                        _arg("dgu", dgu, dev, (rows, 2 * I), act), _arg("h", h, dev, (rows, I), act),
+                                        _arg("dweights", dweights, dev, (T, K), f32), _handle(dh))
     _check(st, "beam_moe_swiglu_backward")
     return dgu, h, dweights
 
@@ -576,21 +606,22 @@ def beam_moe_route_backward(cfg, x, w_router, logits, ids, dweights, dx_add=None
     workspace.  dx may be dx_add itself."""
     import torch
     T, K, H, E, act = _rows_by(x, "x"), cfg.topk, cfg.hidden, cfg.n_experts, _act_torch(cfg)
-    i32, f32 = torch.int32, torch.float32
-    with _On(stream, x, w_router, logits, ids, dweights, dx_add, dx, dw_router, dlogit_bias, ws) as on:
-        dx = torch.empty((T, H), dtype=act, device=on.device) if dx is None else dx
-        dw_router = torch.empty((H, E), dtype=f32, device=on.device) if dw_router is None else dw_router
-        dlogit_bias = torch.empty(E, dtype=f32, device=on.device) if dlogit_bias is None else dlogit_bias
-        if ws is None:
-            need = beam_moe_route_backward_workspace_size(cfg, T)
-            ws = torch.empty(need, dtype=torch.uint8, device=on.device) if need else None
-        st = lib().beam_moe_route_backward(ctypes.byref(cfg), T, _arg("x", x, (T, H), act),
-                                           _arg("w_router", w_router, (H, E), f32), _arg("logits", logits, (T, E), f32),
-                                           _arg("ids", ids, (T, K), i32), _arg("dweights", dweights, (T, K), f32),
-                                           _arg("dx_add", dx_add, (T, H), act), _arg("dx", dx, (T, H), act),
-                                           _arg("dw_router", dw_router, (H, E), f32),
-                                           _arg("dlogit_bias", dlogit_bias, (E,), f32),
-                                           None if ws is None else _ptr(ws),
-                                           0 if ws is None else ws.numel() * ws.element_size(), on.handle)
+    on = _elsewhere(stream, x)
+    if on is not None:
+        with torch.cuda.stream(on):
+            return beam_moe_route_backward(cfg, x, w_router, logits, ids, dweights, dx_add, dx, dw_router, dlogit_bias, ws)
+    f32, dev = torch.float32, x.get_device()
+    dx = x.new_empty((T, H)) if dx is None else dx
+    dw_router = x.new_empty((H, E), dtype=f32) if dw_router is None else dw_router
+    dlogit_bias = x.new_empty(E, dtype=f32) if dlogit_bias is None else dlogit_bias
+    ws, p_ws, n_ws = _temporary(ws, beam_moe_route_backward_workspace_size(cfg, T) if ws is None else 0, x)
+    st = lib().beam_moe_route_backward(ctypes.byref(cfg), T, _arg("x", x, dev, (T, H), act),
+                                       _arg("w_router", w_router, dev, (H, E), f32),
+                                       _arg("logits", logits, dev, (T, E), f32),
+                                       _arg("ids", ids, dev, (T, K), torch.int32),
+                                       _arg("dweights", dweights, dev, (T, K), f32),
+                                       _arg("dx_add", dx_add, dev, (T, H), act), _arg("dx", dx, dev, (T, H), act),
+                                       _arg("dw_router", dw_router, dev, (H, E), f32),
+                                       _arg("dlogit_bias", dlogit_bias, dev, (E,), f32), p_ws, n_ws, _handle(x))
     _check(st, "beam_moe_route_backward")
     return dx, dw_router, dlogit_bias
