@@ -426,9 +426,14 @@ int beam_moe_combine_backward(const beam_moe_config* cfg, int64_t T, const void*
  *   h           device [rows, I] act_dtype out
  *   keep_q      device [rows, 2I] bytes out, keep_scale device [rows, 2, ceil(I/32)] bytes
  *               out: the 8-bit copy of gu, each half blocked on its own; both or neither
+ *   ws          device workspace of ws_bytes >= beam_moe_swiglu_workspace_size(cfg, T, rows);
+ *               0 (NULL is accepted) below 8192 pairs and with row_of_pair NULL
  */
+size_t beam_moe_swiglu_workspace_size(const beam_moe_config* cfg, int64_t T, int64_t rows);
+
 int beam_moe_swiglu(const beam_moe_config* cfg, int64_t T, const void* gu, const int32_t* row_of_pair, int64_t rows,
-                    const float* weights, void* h, uint8_t* keep_q, uint8_t* keep_scale, void* stream);
+                    const float* weights, void* h, uint8_t* keep_q, uint8_t* keep_scale, void* ws, size_t ws_bytes,
+                    void* stream);
 
 /*
  * Gradient of swiglu, s = sigma(g):
@@ -439,10 +444,11 @@ int beam_moe_swiglu(const beam_moe_config* cfg, int64_t T, const void* gu, const
  *   h           device [rows, I] act_dtype out, or NULL: beam_moe_swiglu's result again from
  *               these g and u (the down weights' gradient needs it); may be dh itself
  *   dweights    device [T, K] FP32 out, or NULL; needs weights
+ *   ws          as in beam_moe_swiglu
  */
 int beam_moe_swiglu_backward(const beam_moe_config* cfg, int64_t T, const void* dh, const void* gu,
                              const uint8_t* gu_scale, const int32_t* row_of_pair, int64_t rows, const float* weights,
-                             void* dgu, void* h, float* dweights, void* stream);
+                             void* dgu, void* h, float* dweights, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Gradient of the router: with s_i = sigma(logit of pick i), p_i = s_i / sum_j s_j and

@@ -23,7 +23,7 @@ C_FUNCTIONS = ("beam_moe_status_string", "beam_moe_abi_version", "beam_moe_works
                "beam_moe_sublayer_forward", "beam_moe_time_kernel", "beam_dense_workspace_size",
                "beam_dense_forward", "beam_dense_sublayer_forward", "beam_moe_forward_noalloc",
                "beam_moe_sort_workspace_size", "beam_moe_sort", "beam_moe_dispatch", "beam_moe_dispatch_backward",
-               "beam_moe_combine", "beam_moe_combine_backward", "beam_moe_swiglu", "beam_moe_swiglu_backward",
+               "beam_moe_combine", "beam_moe_combine_backward", "beam_moe_swiglu_workspace_size", "beam_moe_swiglu", "beam_moe_swiglu_backward",
                "beam_moe_route_backward_workspace_size", "beam_moe_route_backward")
 BEAM_KERNEL_NONE, BEAM_KERNEL_ROUTER_LOGITS, BEAM_KERNEL_GATE_UP, BEAM_KERNEL_DOWN, BEAM_KERNEL_COMBINE = range(5)
 
@@ -118,9 +118,11 @@ def lib() -> ctypes.CDLL:
     L.beam_moe_combine_backward.restype = ctypes.c_int
     L.beam_moe_combine_backward.argtypes = [cfgp, i64, vp, vp, vp, i64, vp, vp, vp, vp]
     L.beam_moe_swiglu.restype = ctypes.c_int
-    L.beam_moe_swiglu.argtypes = [cfgp, i64, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.beam_moe_swiglu.argtypes = [cfgp, i64, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.beam_moe_swiglu_workspace_size.restype = sz
+    L.beam_moe_swiglu_workspace_size.argtypes = [cfgp, i64, i64]
     L.beam_moe_swiglu_backward.restype = ctypes.c_int
-    L.beam_moe_swiglu_backward.argtypes = [cfgp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.beam_moe_swiglu_backward.argtypes = [cfgp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
     L.beam_moe_route_backward_workspace_size.restype = sz
     L.beam_moe_route_backward_workspace_size.argtypes = [cfgp, i64]
     L.beam_moe_route_backward.restype = ctypes.c_int
@@ -406,6 +408,18 @@ def route_logits(cfg, T, ws):
     return ws[at:at + 4 * T * cfg.n_experts].view(torch.float32).view(T, cfg.n_experts)
 
 
+def _call(fn, args, ws, need, like):
+    """fn(*args, workspace, its bytes, stream).  Without a workspace of the caller's the call
+    is first made with none, which small ones do not need; only if it asks for one are its
+    need() bytes allocated."""
+    keep, p_ws, n_ws = _temporary(ws, 0, like)
+    st = fn(*args, p_ws, n_ws, _handle(like))
+    if st == BEAM_ERR_WORKSPACE and ws is None:
+        keep, p_ws, n_ws = _temporary(None, need(), like)
+        st = fn(*args, p_ws, n_ws, _handle(like))
+    _check(st, fn.__name__)
+
+
 def beam_moe_sort_workspace_size(cfg: beam_moe_config, T: int) -> int:
     return int(lib().beam_moe_sort_workspace_size(ctypes.byref(cfg), int(T)))
 
@@ -424,15 +438,10 @@ def beam_moe_sort(cfg, ids, expert_off=None, row_of_pair=None, pair_of_row=None,
     expert_off = ids.new_empty(E + 1) if expert_off is None else expert_off
     row_of_pair = ids.new_empty((T, K)) if row_of_pair is None else row_of_pair
     pair_of_row = ids.new_empty(T * K) if pair_of_row is None else pair_of_row
-    fn, c = lib().beam_moe_sort, ctypes.byref(cfg)
-    args = (p_ids, _arg("expert_off", expert_off, dev, (E + 1,), i32), _arg("row_of_pair", row_of_pair, dev, (T, K), i32),
-            _arg("pair_of_row", pair_of_row, dev, (T * K,), i32))
-    ws, p_ws, n_ws = _temporary(ws, 0, ids)
-    st = fn(c, T, *args, p_ws, n_ws, _handle(ids))
-    if st == BEAM_ERR_WORKSPACE and ws is None:            # past one block's pairs
-        ws, p_ws, n_ws = _temporary(None, beam_moe_sort_workspace_size(cfg, T), ids)
-        st = fn(c, T, *args, p_ws, n_ws, _handle(ids))
-    _check(st, "beam_moe_sort")
+    _call(lib().beam_moe_sort, (ctypes.byref(cfg), T, p_ids, _arg("expert_off", expert_off, dev, (E + 1,), i32),
+                                _arg("row_of_pair", row_of_pair, dev, (T, K), i32),
+                                _arg("pair_of_row", pair_of_row, dev, (T * K,), i32)),
+          ws, lambda: beam_moe_sort_workspace_size(cfg, T), ids)
     return expert_off, row_of_pair, pair_of_row
 
 
@@ -537,8 +546,12 @@ def beam_moe_combine_backward(cfg, dy, expert_out, row_of_pair, weights, deo=Non
     return deo, dweights
 
 
+def beam_moe_swiglu_workspace_size(cfg: beam_moe_config, T: int, rows: int) -> int:
+    return int(lib().beam_moe_swiglu_workspace_size(ctypes.byref(cfg), int(T), int(rows)))
+
+
 def beam_moe_swiglu(cfg, gu, weights=None, row_of_pair=None, h=None, keep8=False, keep_q=None, keep_scale=None,
-                    stream=None):
+                    ws=None, stream=None):
     """h[r] = weights[p] * SiLU(g) * u for the rows r of the pairs p, (g, u) the halves of gu
     [rows, 2I]: returns h [rows, I], with keep8 (or keep_q and keep_scale) (h, keep_q,
     keep_scale) with the 8-bit copy of gu.  row_of_pair None: row t for token t (K = 1)."""
@@ -548,7 +561,7 @@ def beam_moe_swiglu(cfg, gu, weights=None, row_of_pair=None, h=None, keep8=False
     on = _elsewhere(stream, gu)
     if on is not None:
         with torch.cuda.stream(on):
-            return beam_moe_swiglu(cfg, gu, weights, row_of_pair, h, keep8, keep_q, keep_scale)
+            return beam_moe_swiglu(cfg, gu, weights, row_of_pair, h, keep8, keep_q, keep_scale, ws)
     u8, f8 = torch.uint8, torch.float8_e4m3fn
     dev, nb = gu.get_device(), keep_blocks(I)
     h = gu.new_empty((rows, I)) if h is None else h
@@ -556,17 +569,17 @@ def beam_moe_swiglu(cfg, gu, weights=None, row_of_pair=None, h=None, keep8=False
         keep_q = gu.new_empty((rows, 2 * I), dtype=f8)
     if keep8 and keep_scale is None:
         keep_scale = gu.new_empty((rows, 2, nb), dtype=u8)
-    st = lib().beam_moe_swiglu(ctypes.byref(cfg), T, _arg("gu", gu, dev, (rows, 2 * I), act),
-                               _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
-                               _arg("weights", weights, dev, (T, K), torch.float32), _arg("h", h, dev, (rows, I), act),
-                               _arg("keep_q", keep_q, dev, (rows, 2 * I), f8, u8),
-                               _arg("keep_scale", keep_scale, dev, (rows, 2, nb), u8), _handle(gu))
-    _check(st, "beam_moe_swiglu")
+    _call(lib().beam_moe_swiglu, (ctypes.byref(cfg), T, _arg("gu", gu, dev, (rows, 2 * I), act),
+                                  _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                  _arg("weights", weights, dev, (T, K), torch.float32),
+                                  _arg("h", h, dev, (rows, I), act), _arg("keep_q", keep_q, dev, (rows, 2 * I), f8, u8),
+                                  _arg("keep_scale", keep_scale, dev, (rows, 2, nb), u8)),
+          ws, lambda: beam_moe_swiglu_workspace_size(cfg, T, rows), gu)
     return h if keep_q is None else (h, keep_q, keep_scale)
 
 
 def beam_moe_swiglu_backward(cfg, dh, gu, gu_scale=None, weights=None, row_of_pair=None, dgu=None, h=None,
-                             dweights=None, again=True, stream=None):
+                             dweights=None, again=True, ws=None, stream=None):
     """Gradients of swiglu from gu, or from its 8-bit copy with gu_scale: (dgu [rows, 2I],
     h [rows, I] computed again, or None with again=False, dweights [T, K], or None without
     weights).  dgu may be gu itself (not a copy), h may be dh itself."""
@@ -576,7 +589,7 @@ def beam_moe_swiglu_backward(cfg, dh, gu, gu_scale=None, weights=None, row_of_pa
     on = _elsewhere(stream, dh)
     if on is not None:
         with torch.cuda.stream(on):
-            return beam_moe_swiglu_backward(cfg, dh, gu, gu_scale, weights, row_of_pair, dgu, h, dweights, again)
+            return beam_moe_swiglu_backward(cfg, dh, gu, gu_scale, weights, row_of_pair, dgu, h, dweights, again, ws)
     u8, f32, dev = torch.uint8, torch.float32, dh.get_device()
     dgu = dh.new_empty((rows, 2 * I)) if dgu is None else dgu
     if again and h is None:
@@ -585,13 +598,13 @@ def beam_moe_swiglu_backward(cfg, dh, gu, gu_scale=None, weights=None, row_of_pa
         dweights = dh.new_empty((T, K), dtype=f32)
     p_gu = _arg("gu", gu, dev, (rows, 2 * I), act) if gu_scale is None else \
         _arg("gu", gu, dev, (rows, 2 * I), torch.float8_e4m3fn, u8)
-    st = lib().beam_moe_swiglu_backward(ctypes.byref(cfg), T, _arg("dh", dh, dev, (rows, I), act), p_gu,
-                                        _arg("gu_scale", gu_scale, dev, (rows, 2, keep_blocks(I)), u8),
-                                        _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
-                                        _arg("weights", weights, dev, (T, K), f32),
-                                        _arg("dgu", dgu, dev, (rows, 2 * I), act), _arg("h", h, dev, (rows, I), act),
-                                        _arg("dweights", dweights, dev, (T, K), f32), _handle(dh))
-    _check(st, "beam_moe_swiglu_backward")
+    _call(lib().beam_moe_swiglu_backward, (ctypes.byref(cfg), T, _arg("dh", dh, dev, (rows, I), act), p_gu,
+                                           _arg("gu_scale", gu_scale, dev, (rows, 2, keep_blocks(I)), u8),
+                                           _arg("row_of_pair", row_of_pair, dev, (T, K), torch.int32), rows,
+                                           _arg("weights", weights, dev, (T, K), f32),
+                                           _arg("dgu", dgu, dev, (rows, 2 * I), act), _arg("h", h, dev, (rows, I), act),
+                                           _arg("dweights", dweights, dev, (T, K), f32)),
+          ws, lambda: beam_moe_swiglu_workspace_size(cfg, T, rows), dh)
     return dgu, h, dweights
 
 

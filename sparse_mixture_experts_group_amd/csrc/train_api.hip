@@ -153,12 +153,36 @@ static int check_swiglu(const beam_moe_config* cfg, int64_t T, const int32_t* ro
 }
 
 static SwigluArgs swiglu_args(const beam_moe_config* c, int64_t T, int64_t rows, const int32_t* row_of_pair,
-                              const float* weights) {
-    return SwigluArgs{T * c->topk, rows, c->inter, c->act_dtype == BEAM_DTYPE_BF16, row_of_pair, weights};
+                              const float* weights, void* ws) {
+    return SwigluArgs{T * c->topk, rows,    c->inter, c->act_dtype == BEAM_DTYPE_BF16,
+                      row_of_pair, weights, static_cast<int32_t*>(ws)};
+}
+
+// Workspace of a SwiGLU call that takes rows in order.
+static size_t swiglu_ws(const beam_moe_config* c, int64_t T, int64_t rows) {
+    return T * c->topk >= kRowOrderPairs ? sizeof(int32_t) * static_cast<size_t>(rows) : 0;
+}
+
+size_t beam_moe_swiglu_workspace_size(const beam_moe_config* cfg, int64_t T, int64_t rows) {
+    if (check_pairs(cfg, T, 1) != BEAM_OK || rows < 0 || rows > INT32_MAX) return 0;
+    return swiglu_ws(cfg, T, rows);
+}
+
+// The call's workspace in *ws (null where it needs none), or an error.
+static int check_swiglu_ws(const beam_moe_config* cfg, int64_t T, int64_t rows, const int32_t* row_of_pair, void** ws,
+                           size_t ws_bytes) {
+    const size_t need = row_of_pair ? swiglu_ws(cfg, T, rows) : 0;
+    if (need == 0) {
+        *ws = nullptr;
+        return BEAM_OK;
+    }
+    if (!*ws || ws_bytes < need) return BEAM_ERR_WORKSPACE;
+    return aligned16(*ws) ? BEAM_OK : BEAM_ERR_INVALID_ARG;
 }
 
 int beam_moe_swiglu(const beam_moe_config* cfg, int64_t T, const void* gu, const int32_t* row_of_pair, int64_t rows,
-                    const float* weights, void* h, uint8_t* keep_q, uint8_t* keep_scale, void* stream) {
+                    const float* weights, void* h, uint8_t* keep_q, uint8_t* keep_scale, void* ws, size_t ws_bytes,
+                    void* stream) {
     int s = check_swiglu(cfg, T, row_of_pair, rows);
     if (s != BEAM_OK) return s;
     if ((keep_q != nullptr) != (keep_scale != nullptr)) return BEAM_ERR_INVALID_ARG;
@@ -166,15 +190,16 @@ int beam_moe_swiglu(const beam_moe_config* cfg, int64_t T, const void* gu, const
     if (!given(gu) || !given(h)) return BEAM_ERR_INVALID_ARG;
     if (!optional(row_of_pair) || !optional(weights) || !optional(keep_q) || !optional(keep_scale))
         return BEAM_ERR_INVALID_ARG;
+    if ((s = check_swiglu_ws(cfg, T, rows, row_of_pair, &ws, ws_bytes)) != BEAM_OK) return s;
     (void)hipGetLastError();
-    launch_swiglu(static_cast<hipStream_t>(stream), swiglu_args(cfg, T, rows, row_of_pair, weights), gu, h, keep_q,
+    launch_swiglu(static_cast<hipStream_t>(stream), swiglu_args(cfg, T, rows, row_of_pair, weights, ws), gu, h, keep_q,
                   keep_scale);
     return launched();
 }
 
 int beam_moe_swiglu_backward(const beam_moe_config* cfg, int64_t T, const void* dh, const void* gu,
                              const uint8_t* gu_scale, const int32_t* row_of_pair, int64_t rows, const float* weights,
-                             void* dgu, void* h, float* dweights, void* stream) {
+                             void* dgu, void* h, float* dweights, void* ws, size_t ws_bytes, void* stream) {
     int s = check_swiglu(cfg, T, row_of_pair, rows);
     if (s != BEAM_OK) return s;
     if (dweights && !weights) return BEAM_ERR_INVALID_ARG;
@@ -182,8 +207,9 @@ int beam_moe_swiglu_backward(const beam_moe_config* cfg, int64_t T, const void* 
     if (rows > 0 && (!given(dh) || !given(gu) || !given(dgu))) return BEAM_ERR_INVALID_ARG;
     if (!optional(gu_scale) || !optional(row_of_pair) || !optional(weights) || !optional(h) || !optional(dweights))
         return BEAM_ERR_INVALID_ARG;
+    if ((s = check_swiglu_ws(cfg, T, rows, row_of_pair, &ws, ws_bytes)) != BEAM_OK) return s;
     (void)hipGetLastError();
-    launch_swiglu_backward(static_cast<hipStream_t>(stream), swiglu_args(cfg, T, rows, row_of_pair, weights), dh, gu,
+    launch_swiglu_backward(static_cast<hipStream_t>(stream), swiglu_args(cfg, T, rows, row_of_pair, weights, ws), dh, gu,
                            gu_scale, dgu, h, dweights);
     return launched();
 }

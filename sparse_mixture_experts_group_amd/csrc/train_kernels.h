@@ -45,7 +45,11 @@ struct SwigluArgs {
     bool bf16;
     const int32_t* row_of_pair;  // [pairs] or null: row = pair
     const float* weights;        // [pairs] or null (ones)
+    int32_t* pair_of_row;        // [rows] of workspace: rows are taken in order; or null: pairs are
 };
+
+// Pairs from which the SwiGLU operators take rows in order (and need the workspace).
+constexpr int64_t kRowOrderPairs = 8192;
 
 void launch_swiglu(hipStream_t st, const SwigluArgs& a, const void* gu, void* h, uint8_t* keep_q, uint8_t* keep_scale);
 // gu_scale: gu holds E4M3 codes.  h and dweights may be null.

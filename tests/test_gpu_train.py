@@ -308,7 +308,8 @@ def test_keep_borders():
 # ---------------------------------------------------------------------------
 SWIGLU = [  # T, I, E, K, drop
     (1, 1, 1, 1, 0), (16, 2560, 256, 8, 0), (5, 7, 3, 2, 0.3), (17, 32, 16, 8, 0.3), (33, 33, 60, 9, 0.2),
-    (40, 257, 16, 6, 0.3), (64, 1001, 7, 3, 0), (300, 504, 256, 8, 0.2), (700, 96, 12, 3, 0.3), (3, 20480, 8, 2, 0.3)]
+    (40, 257, 16, 6, 0.3), (64, 1001, 7, 3, 0), (300, 504, 256, 8, 0.2), (700, 96, 12, 3, 0.3), (3, 20480, 8, 2, 0.3),
+    (1024, 40, 60, 8, 0.2), (1023, 33, 7, 8, 0), (2800, 520, 9, 3, 0.3)]      # 8192 pairs and more: rows in order
 
 
 def swiglu_ref(gu, w, I):

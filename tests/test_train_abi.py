@@ -37,13 +37,13 @@ def combine_backward(c=None, T=4, dy=P, eo=P, row=P, rows=12, w=P, deo=P, dw=P):
     return bm.lib().beam_moe_combine_backward(ctypes.byref(c or cfg()), T, dy, eo, row, rows, w, deo, dw, None)
 
 
-def swiglu(c=None, T=4, gu=P, row=P, rows=12, w=P, h=P, q=None, scale=None):
-    return bm.lib().beam_moe_swiglu(ctypes.byref(c or cfg()), T, gu, row, rows, w, h, q, scale, None)
+def swiglu(c=None, T=4, gu=P, row=P, rows=12, w=P, h=P, q=None, scale=None, ws=None, nb=0):
+    return bm.lib().beam_moe_swiglu(ctypes.byref(c or cfg()), T, gu, row, rows, w, h, q, scale, ws, nb, None)
 
 
-def swiglu_backward(c=None, T=4, dh=P, gu=P, scale=None, row=P, rows=12, w=P, dgu=P, h=P, dw=P):
+def swiglu_backward(c=None, T=4, dh=P, gu=P, scale=None, row=P, rows=12, w=P, dgu=P, h=P, dw=P, ws=None, nb=0):
     return bm.lib().beam_moe_swiglu_backward(ctypes.byref(c or cfg()), T, dh, gu, scale, row, rows, w, dgu, h, dw,
-                                             None)
+                                             ws, nb, None)
 
 
 def route_backward(c=None, T=4, x=P, wr=P, z=P, ids=P, dw=P, add=None, dx=P, dwr=P, db=P, ws=P, nb=BIG):
@@ -133,6 +133,13 @@ def test_swiglu_arguments():
         assert swiglu_backward(**{k: ODD}) == ARG
     assert swiglu_backward(w=None) == ARG                  # gradients of weights that are not there
     assert swiglu(T=0) == OK and swiglu(rows=0, gu=None, h=None) == OK
+    T = 8192 // 3 + 1                                      # from here on rows are taken in order
+    need = bm.beam_moe_swiglu_workspace_size(cfg(), T, 100)
+    assert need >= 400 and bm.beam_moe_swiglu_workspace_size(cfg(), T - 1, 100) == 0
+    assert bm.beam_moe_swiglu_workspace_size(cfg(topk=0), T, 100) == 0
+    for call in (swiglu, swiglu_backward):
+        assert call(T=T, rows=100) == WS and call(T=T, rows=100, ws=P, nb=need - 1) == WS
+        assert call(T=T, rows=100, ws=ODD, nb=need) == ARG
     assert swiglu_backward(T=0, dh=None, gu=None, dgu=None) == OK
 
 
