@@ -5,28 +5,8 @@
 
 namespace beam {
 
-// Item k of a launch.  Items are pairs, or rows where their pairs have been written down
-// (launch_invert).  `row` is where the item's values lie, -1 if nowhere; a row in order is
-// read before its pair is known (`live`: whether it has one), so that no load waits for the
-// look-up.  What stands in pair_of_row for a row without a pair is anything: it counts only
-// if row_of_pair agrees.
-struct Item {
-    int64_t row, pair;
-    bool live;
-};
 __device__ __forceinline__ Item item_at(const SwigluArgs& a, int64_t k) {
-    Item t;
-    if (a.pair_of_row) {
-        t.row = k < a.rows ? k : -1;
-        t.pair = k < a.rows ? a.pair_of_row[k] : -1;
-        t.live = t.pair >= 0 && t.pair < a.pairs && a.row_of_pair[t.pair] == k;
-    } else {
-        t.pair = k;
-        const int64_t r = k >= a.pairs ? -1 : a.row_of_pair ? a.row_of_pair[k] : k;
-        t.live = r >= 0 && r < a.rows;
-        t.row = t.live ? r : -1;
-    }
-    return t;
+    return item_at(k, a.pairs, a.rows, a.row_of_pair, a.pair_of_row);
 }
 
 __device__ __forceinline__ float item_weight(const SwigluArgs& a, const Item& t) {
@@ -35,21 +15,8 @@ __device__ __forceinline__ float item_weight(const SwigluArgs& a, const Item& t)
 
 static int64_t items(const SwigluArgs& a) { return a.pair_of_row ? a.rows : a.pairs; }
 
-// pair_of_row from row_of_pair; a dropped pair's dweights are zeros.  Taking the rows in
-// order, one stream of addresses an array instead of one an expert, is worth this pass of 8
-// bytes a pair: 65536 rows of 2560 columns took 268 us forward and 340 us backward in the
-// order of pairs, 219 and 270 us in the order of rows.
-__global__ __launch_bounds__(256) void invert_rows(SwigluArgs a, float* __restrict__ dweights) {
-    const int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (p >= a.pairs) return;
-    const int64_t r = a.row_of_pair[p];
-    if (r >= 0 && r < a.rows) a.pair_of_row[r] = static_cast<int32_t>(p);
-    else if (dweights) dweights[p] = 0.0f;
-}
-
-static void launch_invert(hipStream_t st, const SwigluArgs& a, float* dweights) {
-    if (a.pair_of_row)
-        invert_rows<<<static_cast<unsigned>((a.pairs + 255) / 256), 256, 0, st>>>(a, dweights);
+static void write_pairs_down(hipStream_t st, const SwigluArgs& a, float* dweights) {
+    if (a.pair_of_row) launch_invert(st, a.pairs, a.rows, a.row_of_pair, a.pair_of_row, dweights);
 }
 
 // sigma(g): the hardware exponential and reciprocal, about 2 ulp; results are rounded to
@@ -106,7 +73,7 @@ static void swiglu_typed(hipStream_t st, const SwigluArgs& a, const void* gu, vo
                          uint8_t* keep_scale) {
     const int pieces = (a.I + 31) / 32 * 4;
     const unsigned blocks = static_cast<unsigned>((items(a) * pieces + 255) / 256);
-    launch_invert(st, a, nullptr);
+    write_pairs_down(st, a, nullptr);
     if (keep_q) swiglu_rows<BF16, ALIGNED, true><<<blocks, 256, 0, st>>>(a, pieces, gu, h, keep_q, keep_scale);
     else swiglu_rows<BF16, ALIGNED, false><<<blocks, 256, 0, st>>>(a, pieces, gu, h, nullptr, nullptr);
 }
@@ -223,9 +190,11 @@ __global__ __launch_bounds__(1024) void swiglu_backward(SwigluArgs a, int group,
 template <bool BF16, bool ALIGNED, bool SRC8>
 static void swiglu_backward_typed(hipStream_t st, const SwigluArgs& a, const void* dh, const void* gu,
                                   const uint8_t* gu_scale, void* dgu, void* h, float* dweights) {
-    launch_invert(st, a, dweights);
+    write_pairs_down(st, a, dweights);
     if (dweights) {
-        const int group = row_group(a.I);
+        // 65536 rows of 2560 columns: 299 us with a piece a thread (320 threads), 349 with a
+        // wave a row; rows in order keep even large blocks' addresses close together
+        const int group = row_group(a.I, 1024);
         swiglu_backward<BF16, ALIGNED, SRC8><<<group_blocks(items(a), group), group_threads(group), 0, st>>>(
             a, group, dh, gu, gu_scale, dgu, h, dweights);
     } else {

@@ -19,6 +19,14 @@ void launch_sort_pairs(hipStream_t st, int64_t pairs, int E, const int32_t* ids,
                        int32_t* row_of_pair, int32_t* pair_of_row, int32_t* counts, int32_t* totals);
 
 // ---- rows (dispatch.hip) --------------------------------------------------
+// Pairs from which the SwiGLU operators take rows in order; they need a workspace of an
+// int32 a row then.
+constexpr int64_t kRowOrderPairs = 8192;
+
+// pair_of_row [rows] from row_of_pair [pairs]; a dropped pair's dweights (if given) are zeros.
+void launch_invert(hipStream_t st, int64_t pairs, int64_t rows, const int32_t* row_of_pair, int32_t* pair_of_row,
+                   float* dweights);
+
 struct RowArgs {
     int64_t T;                   // tokens
     int64_t rows;                // rows of the sorted buffers
@@ -48,8 +56,6 @@ struct SwigluArgs {
     int32_t* pair_of_row;        // [rows] of workspace: rows are taken in order; or null: pairs are
 };
 
-// Pairs from which the SwiGLU operators take rows in order (and need the workspace).
-constexpr int64_t kRowOrderPairs = 8192;
 
 void launch_swiglu(hipStream_t st, const SwigluArgs& a, const void* gu, void* h, uint8_t* keep_q, uint8_t* keep_scale);
 // gu_scale: gu holds E4M3 codes.  h and dweights may be null.

@@ -225,6 +225,31 @@ __device__ __forceinline__ float group_sum(float v, int group, float* s_part) {
     return v;
 }
 
+// Item k of a launch over pairs or, where their pairs have been written down
+// (launch_invert), over rows.  `row` is where the item's values lie, -1 if nowhere; a row in
+// order is read before its pair is known (`live`: whether it has one), so that no load waits
+// for the look-up.  What stands in pair_of_row for a row without a pair is anything: it
+// counts only if row_of_pair agrees.
+struct Item {
+    int64_t row, pair;
+    bool live;
+};
+__device__ __forceinline__ Item item_at(int64_t k, int64_t pairs, int64_t rows, const int32_t* row_of_pair,
+                                        const int32_t* pair_of_row) {
+    Item t;
+    if (pair_of_row) {
+        t.row = k < rows ? k : -1;
+        t.pair = k < rows ? pair_of_row[k] : -1;
+        t.live = t.pair >= 0 && t.pair < pairs && row_of_pair[t.pair] == k;
+    } else {
+        t.pair = k;
+        const int64_t r = k >= pairs ? -1 : row_of_pair ? row_of_pair[k] : k;
+        t.live = r >= 0 && r < rows;
+        t.row = t.live ? r : -1;
+    }
+    return t;
+}
+
 // Thread -> (row, 8-column piece) with rows packed back to back over the grid, so that
 // narrow rows leave no lanes idle.  `pieces` per row; block b covers pieces 256 b ..
 // 256 b + 255.  The division of a block's first piece is uniform; a thread's own is at
@@ -242,12 +267,10 @@ __device__ __forceinline__ void piece_of_thread(int pieces, int64_t& row, int& p
 
 // Threads that share a row in the kernels that add over it: a lane for each 8-column piece,
 // a power of two up to a wave (several rows a block of 256), or a block of whole waves (one
-// row a block, up to 1024 threads).  A thread that takes one piece keeps the addresses in
-// flight close together: 8192 tokens' gradient of combine ran at 4.9 TB/s with a wave
-// walking a token's ten pieces a lane, and at 5.8 with a block a token.
-inline int row_group(int cols) {
+// row a block) of at most `most` threads, a multiple of 64 up to 1024.
+inline int row_group(int cols, int most) {
     const int pieces = (cols + 7) / 8;
-    if (pieces > 64) return pieces >= 1024 ? 1024 : (pieces + 63) / 64 * 64;
+    if (pieces > 64) return pieces >= most ? most : (pieces + 63) / 64 * 64;
     int g = 8;
     while (g < pieces) g *= 2;
     return g;
