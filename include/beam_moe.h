@@ -367,7 +367,7 @@ int beam_moe_forward_noalloc(const beam_moe_config* cfg, int64_t T, const void* 
  *   row_of_pair device [T, K] int32 out: row of each pair, -1 if dropped
  *   pair_of_row device [T*K] int32 out: pair of each row, -1 from row expert_off[E] on
  *   ws          device workspace of ws_bytes >= beam_moe_sort_workspace_size(cfg, T),
- *               which is 0 (NULL is accepted) up to 8192 pairs
+ *               which is 0 (NULL is accepted) up to 4096 pairs
  * T == 0 writes expert_off (zeros).
  */
 size_t beam_moe_sort_workspace_size(const beam_moe_config* cfg, int64_t T);

@@ -23,19 +23,19 @@ __device__ __forceinline__ uint64_t same_expert(int e, uint64_t valid) {
     return m;
 }
 
-// Counts of a chunk's experts.
-__global__ __launch_bounds__(256) void sort_count(int64_t pairs, int E, const int32_t* __restrict__ ids,
+// Counts of a chunk's experts (256 of them; those past E stay 0).
+__global__ __launch_bounds__(256) void sort_count(int64_t pairs, int64_t chunk, int E, const int32_t* __restrict__ ids,
                                                   int32_t* __restrict__ counts) {
     __shared__ int s_cnt[kMaxExperts];
     s_cnt[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kSortChunk;
-    for (int j = threadIdx.x; j < kSortChunk; j += 256) {
-        const int e = p0 + j < pairs ? ids[p0 + j] : -1;
+    const int64_t p0 = chunk * blockIdx.x, p1 = p0 + chunk < pairs ? p0 + chunk : pairs;
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += 256) {
+        const int e = ids[p];
         if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
     }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < E) counts[static_cast<int64_t>(blockIdx.x) * E + threadIdx.x] = s_cnt[threadIdx.x];
+    counts[blockIdx.x * kMaxExperts + threadIdx.x] = s_cnt[threadIdx.x];
 }
 
 // Exclusive prefix sum over the first 256 threads' values (thread order), and the total.
@@ -62,63 +62,59 @@ __device__ __forceinline__ int scan256(int v, int* sh, int& total) {
     return before + x - v;
 }
 
-// Block e: counts of expert e in chunk order -> rows of that expert before each chunk
-// (in place), and its total.
-__global__ __launch_bounds__(256) void sort_scan(int64_t nblk, int E, int32_t* __restrict__ counts,
-                                                 int32_t* __restrict__ totals) {
-    __shared__ int sh[4];
-    const int e = blockIdx.x;
-    int carry = 0;
-    for (int64_t b0 = 0; b0 < nblk; b0 += 256) {
-        const int64_t b = b0 + threadIdx.x;
-        const int v = b < nblk ? counts[b * E + e] : 0;
-        int tot;
-        const int ex = scan256(v, sh, tot);
-        if (b < nblk) counts[b * E + e] = carry + ex;
-        carry += tot;
-    }
-    if (threadIdx.x == 0) totals[e] = carry;
-}
-
 // Ranks and writes one chunk.  Each of the NW waves owns a contiguous part of it: counts
-// of its part first, then, with the offsets of the waves before it, each group of 64 pairs
-// in order (rank inside the group from same_expert).  SINGLE: the chunk is the batch, and
-// the expert offsets come from its own counts.
+// of its part first, then, with the offsets of the chunks and waves before it, each group of
+// 64 pairs in order (rank inside the group from same_expert).  SINGLE: the chunk is the
+// batch, and the expert offsets come from its own counts; otherwise every block adds up all
+// chunks' counts (at most 256 KB out of L2) rather than wait for another launch.
 template <int NW, bool SINGLE>
-__global__ __launch_bounds__(NW * 64) void sort_scatter(int64_t pairs, int E, const int32_t* __restrict__ ids,
-                                                        const int32_t* __restrict__ before,
-                                                        const int32_t* __restrict__ totals,
+__global__ __launch_bounds__(NW * 64) void sort_scatter(int64_t pairs, int64_t chunk, int E,
+                                                        const int32_t* __restrict__ ids,
+                                                        const int32_t* __restrict__ counts,
                                                         int32_t* __restrict__ expert_off,
                                                         int32_t* __restrict__ row_of_pair,
                                                         int32_t* __restrict__ pair_of_row) {
+    static_assert(NW >= 4, "a thread an expert");
     __shared__ int s_at[NW][kMaxExperts];     // counts, then the next row, per wave and expert
+    __shared__ __attribute__((aligned(16))) int s_all[SINGLE ? 1 : 2 * NW][kMaxExperts];
     __shared__ int sh[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t p0 = SINGLE ? 0 : static_cast<int64_t>(blockIdx.x) * kSortChunk;
-    const int n = static_cast<int>(SINGLE ? pairs : (pairs - p0 < kSortChunk ? pairs - p0 : kSortChunk));
-    const int part = ((n + NW - 1) / NW + 63) / 64 * 64;
-    const int lo = wave * part, hi = lo + part < n ? lo + part : n;
+    const int64_t p0 = SINGLE ? 0 : chunk * blockIdx.x;
+    const int64_t n = SINGLE ? pairs : (pairs - p0 < chunk ? pairs - p0 : chunk);
+    const int64_t part = ((n + NW - 1) / NW + 63) / 64 * 64;
+    const int64_t lo = wave * part, hi = lo + part < n ? lo + part : n;
     for (int i = tid; i < NW * kMaxExperts; i += NW * 64) s_at[0][i] = 0;
+    if constexpr (!SINGLE) {                  // a lane four experts, a wave every NWth chunk
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        i32x4 before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+        const int nblk = gridDim.x;
+#pragma unroll 8
+        for (int b = wave; b < nblk; b += NW) {
+            const i32x4 v = *reinterpret_cast<const i32x4*>(counts + b * kMaxExperts + lane * 4);
+            all += v;
+            before += b < static_cast<int>(blockIdx.x) ? v : i32x4{0, 0, 0, 0};
+        }
+        *reinterpret_cast<i32x4*>(&s_all[wave][lane * 4]) = all;
+        *reinterpret_cast<i32x4*>(&s_all[NW + wave][lane * 4]) = before;
+    }
     __syncthreads();
-    for (int j = lo + lane; j < hi; j += 64) {
+    for (int64_t j = lo + lane; j < hi; j += 64) {
         const int e = ids[p0 + j];
         if (e >= 0 && e < E) atomicAdd(&s_at[wave][e], 1);
     }
     __syncthreads();
-    int count = 0;
+    int count = 0, at = 0;
     if (tid < E) {
-        if constexpr (SINGLE) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w) count += s_at[w][tid];
-        } else {
-            count = totals[tid];
+        for (int w = 0; w < NW; ++w) {
+            count += SINGLE ? s_at[w][tid] : s_all[w][tid];
+            if constexpr (!SINGLE) at += s_all[NW + w][tid];
         }
     }
     int live;                                 // rows in all
     const int off = scan256(count, sh, live);
     if (tid < E) {
-        int at = off;
-        if constexpr (!SINGLE) at += before[static_cast<int64_t>(blockIdx.x) * E + tid];
+        at += off;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const int c = s_at[w][tid];
@@ -129,8 +125,8 @@ __global__ __launch_bounds__(NW * 64) void sort_scatter(int64_t pairs, int E, co
     }
     if (blockIdx.x == 0 && tid == 0) expert_off[E] = live;
     __syncthreads();
-    for (int j0 = lo; j0 < hi; j0 += 64) {    // wave-uniform bounds
-        const int j = j0 + lane;
+    for (int64_t j0 = lo; j0 < hi; j0 += 64) {    // wave-uniform bounds
+        const int64_t j = j0 + lane;
         const int e = j < hi ? ids[p0 + j] : -1;
         const bool ok = e >= 0 && e < E;
         const uint64_t same = same_expert(e, wave_ballot(ok));
@@ -147,25 +143,24 @@ __global__ __launch_bounds__(NW * 64) void sort_scatter(int64_t pairs, int E, co
         __builtin_amdgcn_wave_barrier();
     }
     // rows behind the last one belong to no pair
-    for (int j = tid; j < n; j += NW * 64)
+    for (int64_t j = tid; j < n; j += NW * 64)
         if (p0 + j >= live) pair_of_row[p0 + j] = -1;
 }
 
 void launch_sort_pairs(hipStream_t st, int64_t pairs, int E, const int32_t* ids, int32_t* expert_off,
-                       int32_t* row_of_pair, int32_t* pair_of_row, int32_t* counts, int32_t* totals) {
+                       int32_t* row_of_pair, int32_t* pair_of_row, int32_t* counts) {
     const int64_t nblk = sort_blocks(pairs);
     if (nblk == 0) {
         // a few pairs need no sixteen waves' counters
         if (pairs <= 512)
-            sort_scatter<4, true><<<1, 256, 0, st>>>(pairs, E, ids, nullptr, nullptr, expert_off, row_of_pair, pair_of_row);
+            sort_scatter<4, true><<<1, 256, 0, st>>>(pairs, 0, E, ids, nullptr, expert_off, row_of_pair, pair_of_row);
         else
-            sort_scatter<16, true><<<1, 1024, 0, st>>>(pairs, E, ids, nullptr, nullptr, expert_off, row_of_pair,
-                                                       pair_of_row);
+            sort_scatter<16, true><<<1, 1024, 0, st>>>(pairs, 0, E, ids, nullptr, expert_off, row_of_pair, pair_of_row);
         return;
     }
-    sort_count<<<static_cast<unsigned>(nblk), 256, 0, st>>>(pairs, E, ids, counts);
-    sort_scan<<<E, 256, 0, st>>>(nblk, E, counts, totals);
-    sort_scatter<4, false><<<static_cast<unsigned>(nblk), 256, 0, st>>>(pairs, E, ids, counts, totals, expert_off,
+    const int64_t chunk = sort_chunk(pairs);
+    sort_count<<<static_cast<unsigned>(nblk), 256, 0, st>>>(pairs, chunk, E, ids, counts);
+    sort_scatter<4, false><<<static_cast<unsigned>(nblk), 256, 0, st>>>(pairs, chunk, E, ids, counts, expert_off,
                                                                         row_of_pair, pair_of_row);
 }
 

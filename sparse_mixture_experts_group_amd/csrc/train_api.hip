@@ -47,10 +47,7 @@ RowArgs row_args(const beam_moe_config* c, int64_t T, int64_t rows, const int32_
 
 int launched() { return hipGetLastError() == hipSuccess ? BEAM_OK : BEAM_ERR_HIP; }
 
-size_t sort_ws(int64_t pairs, int E) {
-    const int64_t nblk = sort_blocks(pairs);
-    return nblk == 0 ? 0 : sizeof(int32_t) * static_cast<size_t>(nblk + 1) * E;
-}
+size_t sort_ws(int64_t pairs) { return sizeof(int32_t) * static_cast<size_t>(sort_blocks(pairs)) * kMaxExperts; }
 
 int check_experts(const beam_moe_config* c) {
     return c->n_experts >= 1 && c->n_experts <= kMaxExperts ? BEAM_OK : BEAM_ERR_INVALID_ARG;
@@ -62,7 +59,7 @@ extern "C" {
 
 size_t beam_moe_sort_workspace_size(const beam_moe_config* cfg, int64_t T) {
     if (check_pairs(cfg, T, 1) != BEAM_OK || check_experts(cfg) != BEAM_OK) return 0;
-    return sort_ws(T * cfg->topk, cfg->n_experts);
+    return sort_ws(T * cfg->topk);
 }
 
 int beam_moe_sort(const beam_moe_config* cfg, int64_t T, const int32_t* ids, int32_t* expert_off,
@@ -73,16 +70,14 @@ int beam_moe_sort(const beam_moe_config* cfg, int64_t T, const int32_t* ids, int
     if (!given(expert_off)) return BEAM_ERR_INVALID_ARG;
     if (T > 0 && (!given(ids) || !given(row_of_pair) || !given(pair_of_row))) return BEAM_ERR_INVALID_ARG;
     const int64_t pairs = T * cfg->topk;
-    const size_t need = sort_ws(pairs, cfg->n_experts);
+    const size_t need = sort_ws(pairs);
     if (need > 0) {
         if (!ws || ws_bytes < need) return BEAM_ERR_WORKSPACE;
         if (!aligned16(ws)) return BEAM_ERR_INVALID_ARG;
     }
-    int32_t* counts = static_cast<int32_t*>(ws);
-    int32_t* totals = need > 0 ? counts + sort_blocks(pairs) * cfg->n_experts : nullptr;
     (void)hipGetLastError();
     launch_sort_pairs(static_cast<hipStream_t>(stream), pairs, cfg->n_experts, ids, expert_off, row_of_pair,
-                      pair_of_row, counts, totals);
+                      pair_of_row, static_cast<int32_t*>(ws));
     return launched();
 }
 

@@ -97,7 +97,7 @@ def restore(codes, scale, C):
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("T,E,K,drop,skew", [
     (1, 1, 1, 0, False), (1, 256, 8, 0, False), (3, 2, 1, 0.5, False), (64, 256, 8, 0, False), (65, 60, 8, 0.3, False),
-    (512, 3, 1, 0, False), (513, 256, 1, 0.1, True), (1024, 256, 8, 0, True), (1025, 255, 8, 0.2, False),
+    (512, 3, 1, 0, False), (513, 256, 1, 0.1, True), (512, 256, 8, 0, True), (513, 255, 8, 0.1, False), (1024, 256, 8, 0, True), (1025, 255, 8, 0.2, False),
     (2731, 2, 3, 0, True), (4099, 256, 8, 0.1, True), (700, 256, 32, 0.05, False), (20001, 17, 5, 0.4, True),
     (66000, 256, 8, 0, False)])
 def test_sort(T, E, K, drop, skew):

@@ -92,9 +92,9 @@ def test_sort_arguments():
     for k in ("ids", "off", "row", "pair"):
         assert sort(**{k: None}) == ARG and sort(**{k: ODD}) == ARG
     assert sort(T=0, off=None) == ARG                      # the offsets of no pairs are written
-    big = 8192 // 3 + 1
+    big = 4096 // 3 + 1
     need = bm.beam_moe_sort_workspace_size(cfg(), big)
-    assert bm.beam_moe_sort_workspace_size(cfg(), 8192 // 3) == 0 and need > 0
+    assert bm.beam_moe_sort_workspace_size(cfg(), 4096 // 3) == 0 and need > 0
     assert sort(T=big) == WS
     assert sort(T=big, ws=P, nb=need - 1) == WS
     assert sort(T=big, ws=ODD, nb=need) == ARG
