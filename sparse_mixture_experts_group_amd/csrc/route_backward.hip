@@ -40,7 +40,7 @@ RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K) {
     p.expert = take(sizeof(int32_t) * T * K);
     p.split = take(8 * T * K);
     p.live = take(T + 8);                      // read eight at a time
-    p.part = take(sizeof(float) * p.splits * (static_cast<size_t>(H) + 1) * E);
+    p.part = take(p.splits > 1 ? sizeof(float) * p.splits * (static_cast<size_t>(H) + 1) * E : 0);
     p.total = off;
     return p;
 }
@@ -172,19 +172,6 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
                                                  const void* dx_add, void* dx) {
     extern __shared__ __attribute__((aligned(16))) float s_w[];
     const int c0 = blockIdx.x * kColTile;
-    const int size = (a.H - c0 < kColTile ? a.H - c0 : kColTile) * a.E;
-    const float* w0 = wr + static_cast<int64_t>(c0) * a.E;
-    for (int j0 = threadIdx.x; j0 < size; j0 += 8 * 1024) {      // eight loads in flight
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = w0[j0 + 1024 * k < size ? j0 + 1024 * k : 0];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int j = j0 + 1024 * k, col = j / a.E;
-            if (j < size) s_w[(j - col * a.E) * kDxStride + col] = v[k];
-        }
-    }
-    __syncthreads();
     static_assert(KT <= 16, "one pick a lane");
     constexpr int NP = KT > 0 ? 1 : 2;                 // picks a lane
     const int K = KT > 0 ? KT : a.K;
@@ -215,6 +202,19 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
     constexpr int kStride = 16 * 4 * kDxStep;          // tokens of the block's sixteen waves
     int64_t t = t0 + wave * 4 * kDxStep;
     if (t < t1) fetch(t);
+    // W's columns, a wave every sixteenth: eight loads in flight
+    const int cols = a.H - c0 < kColTile ? a.H - c0 : kColTile;
+    for (int ee = lane; ee < a.E; ee += 64) {
+        float w[kColTile / 16];
+#pragma unroll
+        for (int k = 0; k < kColTile / 16; ++k) {
+            const int col = wave + 16 * k;
+            w[k] = wr[static_cast<int64_t>(c0 + (col < cols ? col : 0)) * a.E + ee];
+        }
+#pragma unroll
+        for (int k = 0; k < kColTile / 16; ++k) s_w[ee * kDxStride + wave + 16 * k] = w[k];
+    }
+    __syncthreads();
     for (; t < t1; t += kStride) {
 #pragma unroll
         for (int s = 0; s < kDxStep; ++s) {
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
 // after the products.  One buffer: two blocks share a CU (57 KB each for 256 experts and
 // BF16), and one's products run while the other writes its stage.  A stage's values are
 // loaded into registers a stage ahead.  Token ranges (blockIdx.y) write partial sums
-// [H+1, E].
+// [H+1, E], a single range the gradients themselves.
 template <bool BF16, int ME, int Q_>
 struct DwTile {
     static constexpr int W = 4, kThreads = W * 64;       // waves, threads
@@ -300,7 +300,8 @@ __device__ __forceinline__ int dz_offset(int e, int k, int chunk) {
 template <bool BF16, bool EVEN, int ME, int Q_>
 __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t per_split, const void* __restrict__ x,
                                                    const u32x2* __restrict__ split, const uint8_t* __restrict__ alive,
-                                                   float* __restrict__ part) {
+                                                   float* __restrict__ part, float* __restrict__ dw,
+                                                   float* __restrict__ dbias) {
     using L = DwTile<BF16, ME, Q_>;
     extern __shared__ __attribute__((aligned(16))) char s_stage[];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -458,7 +459,10 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
     for (int j = 0; j < L::TN; ++j) {
         const int c = c0 + wn * L::NW + j * 32 + (lane & 31);
         if (c > a.H) continue;
-        float* out = part + (static_cast<int64_t>(blockIdx.y) * (a.H + 1) + c) * a.E;
+        float* out;
+        if (gridDim.y > 1) out = part + (static_cast<int64_t>(blockIdx.y) * (a.H + 1) + c) * a.E;
+        else out = c < a.H ? dw + static_cast<int64_t>(c) * a.E : dbias;
+        if (!out) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -501,25 +505,26 @@ static void dx_launch(hipStream_t st, const RouteBackwardArgs& a, const float* w
 
 template <bool BF16, bool EVEN, int ME, int Q>
 static void dw_launch_picks(hipStream_t st, const RouteBackwardArgs& a, int splits, const void* x, const u32x2* split,
-                            const uint8_t* alive, float* part) {
+                            const uint8_t* alive, float* part, float* dw, float* dbias) {
     using L = DwTile<BF16, ME, Q>;
     const int64_t per = ((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens;
     lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16, EVEN, ME, Q>), L::kLds);
     route_dw<BF16, EVEN, ME, Q><<<dim3((a.H + kDwCols) / kDwCols, splits), L::kThreads, L::kLds, st>>>(
-        a, per, x, split, alive, part);
+        a, per, x, split, alive, part, dw, dbias);
 }
 
 template <bool BF16, bool EVEN, int ME>
 static void dw_launch(hipStream_t st, const RouteBackwardArgs& a, int splits, const void* x, const u32x2* split,
-                      const uint8_t* alive, float* part) {
-    if (a.K <= 8) dw_launch_picks<BF16, EVEN, ME, 1>(st, a, splits, x, split, alive, part);
-    else dw_launch_picks<BF16, EVEN, ME, 4>(st, a, splits, x, split, alive, part);
+                      const uint8_t* alive, float* part, float* dw, float* dbias) {
+    if (a.K <= 8) dw_launch_picks<BF16, EVEN, ME, 1>(st, a, splits, x, split, alive, part, dw, dbias);
+    else dw_launch_picks<BF16, EVEN, ME, 4>(st, a, splits, x, split, alive, part, dw, dbias);
 }
 
 template <bool BF16, bool EVEN>
 static void route_backward_typed(hipStream_t st, const RouteBackwardArgs& a, const RouteBackwardPlan& p, const void* x,
                                  const float* w_router, const void* dx_add, void* dx, const float* dz,
-                                 const int32_t* expert, const u32x2* split, const uint8_t* alive, float* part) {
+                                 const int32_t* expert, const u32x2* split, const uint8_t* alive, float* part,
+                                 float* dw, float* dbias) {
     if (dx) {
         const bool al = a.H % 8 == 0;
         if (al && a.K == 8) dx_launch<BF16, true, 8>(st, a, w_router, dz, expert, dx_add, dx);
@@ -527,9 +532,9 @@ static void route_backward_typed(hipStream_t st, const RouteBackwardArgs& a, con
         else dx_launch<BF16, false, 0>(st, a, w_router, dz, expert, dx_add, dx);
     }
     const int me = dw_experts(a.E);
-    if (me == 64) dw_launch<BF16, EVEN, 64>(st, a, p.splits, x, split, alive, part);
-    else if (me == 128) dw_launch<BF16, EVEN, 128>(st, a, p.splits, x, split, alive, part);
-    else dw_launch<BF16, EVEN, 256>(st, a, p.splits, x, split, alive, part);
+    if (me == 64) dw_launch<BF16, EVEN, 64>(st, a, p.splits, x, split, alive, part, dw, dbias);
+    else if (me == 128) dw_launch<BF16, EVEN, 128>(st, a, p.splits, x, split, alive, part, dw, dbias);
+    else dw_launch<BF16, EVEN, 256>(st, a, p.splits, x, split, alive, part, dw, dbias);
 }
 
 void launch_route_backward(hipStream_t st, const RouteBackwardArgs& a, const RouteBackwardPlan& p, const void* x,
@@ -549,7 +554,9 @@ void launch_route_backward(hipStream_t st, const RouteBackwardArgs& a, const Rou
         const bool even = a.H % 2 == 0;
         const auto run = a.bf16 ? (even ? &route_backward_typed<true, true> : &route_backward_typed<true, false>)
                                 : (even ? &route_backward_typed<false, true> : &route_backward_typed<false, false>);
-        run(st, a, p, x, w_router, dx_add, dx, dz, expert, reinterpret_cast<const u32x2*>(split), alive, part);
+        run(st, a, p, x, w_router, dx_add, dx, dz, expert, reinterpret_cast<const u32x2*>(split), alive, part,
+            dw_router, dlogit_bias);
+        if (p.splits == 1) return;
     }
     const int64_t slice = (static_cast<int64_t>(a.H) + 1) * a.E;
     route_dw_sum<<<static_cast<unsigned>((slice + 255) / 256), 256, 0, st>>>(

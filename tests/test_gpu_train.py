@@ -730,3 +730,27 @@ def test_binding_refuses_wrong_tensors():
         bm.beam_moe_route_backward(cfg, x, torch.zeros((64, 4), device="cuda"), torch.zeros((3, 4), device="cuda"), ids, w,
                                    ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [1, 64, 65, 130])
+def test_route_backward_without_parts(T):
+    """One token range writes the gradients themselves, several write parts that are added:
+    both sides of that border, and without the bias' gradient at the C entry."""
+    import ctypes
+    H, E, K = 200, 33, 3
+    cfg = config("f32", H=H, E=E, K=K, alpha=1.75)
+    ids, z, gw, x, wr = picks(T, T, E, K), rand(1, T, E), rand(2, T, K), rand(3, T, H), rand(5, H, E)
+    ref = route_ref(f64(x), f64(wr), f64(z), ids.numpy(), f64(gw), np.zeros((T, H)), 1.75)
+    d = [t.cuda() for t in (x, wr, z, ids, gw)]
+    dx, dwr, db = bm.beam_moe_route_backward(cfg, *d)
+    rdz = (K + 24) * 2.0 ** -23
+    within(dwr, ref[1], (rdz + (T + 8) * U) * ref[4], "dw_router")
+    within(db, ref[2], (rdz + (T + 8) * U) * ref[5], "dlogit_bias")
+    ws = torch.empty(bm.beam_moe_route_backward_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+    again = torch.zeros_like(dwr)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    st = bm.lib().beam_moe_route_backward(ctypes.byref(cfg), T, *(p(t) for t in d), None, None, p(again), None, p(ws),
+                                          ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == bm.BEAM_OK
+    torch.cuda.synchronize()
+    assert torch.equal(again, dwr)
