@@ -276,7 +276,10 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
 // after the products.  One buffer: two blocks share a CU (57 KB each for 256 experts and
 // BF16), and one's products run while the other writes its stage.  A stage's values are
 // loaded into registers a stage ahead.  Token ranges (blockIdx.y) write partial sums
-// [H+1, E], a single range the gradients themselves.
+// [H+1, E], a single range the gradients themselves.  Matrix-bound: the three (FP32: six)
+// products of 32768 tokens (8192) run at 1.35 PFLOP/s, where a large library product in
+// BF16 reaches 1.24; the same sums as FP32 additions in LDS, a lane a column, took 9.7 ms
+// where this takes 0.2.
 template <bool BF16, int ME, int Q_>
 struct DwTile {
     static constexpr int W = 4, kThreads = W * 64;       // waves, threads
@@ -298,7 +301,7 @@ __device__ __forceinline__ int dz_offset(int e, int k, int chunk) {
 }
 
 template <bool BF16, bool EVEN, int ME, int Q_>
-__global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t per_split, const void* __restrict__ x,
+__global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int per_split, const void* __restrict__ x,
                                                    const u32x2* __restrict__ split, const uint8_t* __restrict__ alive,
                                                    float* __restrict__ part, float* __restrict__ dw,
                                                    float* __restrict__ dbias) {
@@ -308,8 +311,8 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % L::WM, wn = wave / L::WM;
     const int c0 = blockIdx.x * kDwCols, col = lane * 2;
-    const int64_t t0 = per_split * blockIdx.y;
-    const int64_t t1 = t0 + per_split < a.T ? t0 + per_split : a.T;
+    const int t0 = per_split * blockIdx.y;     // T, and T * K, are below 2^30
+    const int t1 = t0 + per_split < a.T ? t0 + per_split : static_cast<int>(a.T);
     for (int j = tid; j < L::kLds / 16; j += L::kThreads) reinterpret_cast<u32x4*>(s_stage)[j] = u32x4{0, 0, 0, 0};
 
     struct Stage {
@@ -332,17 +335,25 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
         chunk[q] = tok >> 3;
         byte[q] = (tok & 7) * 2;
     }
-    const int64_t end = t1 * a.K;
-    auto fetch = [&](Stage& f, int64_t t) {
-        const int64_t tw = t + wave * L::TPW;                    // a multiple of 8
-        f.live = *reinterpret_cast<const u32x2*>(alive + (tw < t1 ? tw : t0));
+    const int end = t1 * a.K;
+    // A zero that the compiler cannot tell for the same in all lanes: `alive` is then read by
+    // a vector load.  A scalar one shares its counter with the LDS reads, whose waits would
+    // wait for it too.
+    int zero;
+    asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
+    const uint32_t row_bytes = static_cast<uint32_t>(a.H) * (BF16 ? 2 : 4);
+    auto fetch = [&](Stage& f, int t) {
+        const int tw = t + wave * L::TPW, first = tw < t1 ? tw : t1 - 1, rest = t1 - 1 - first;
+        // first is a multiple of 8, or past the range and of no account
+        f.live = *reinterpret_cast<const u32x2*>(alive + (first & ~7) + zero);
+        const char* row = static_cast<const char*>(x) + static_cast<int64_t>(first) * row_bytes;
 #pragma unroll
         for (int j = 0; j < L::TPW; ++j)
-            f.x[j] = load2<BF16, EVEN>(row_at<BF16>(x, tw + j < t1 ? tw + j : t1 - 1, a.H), a.H, c0 + col);
+            f.x[j] = load2<BF16, EVEN>(row + (j < rest ? j : rest) * row_bytes, a.H, c0 + col);
 #pragma unroll
         for (int q = 0; q < L::Q; ++q) {
-            const int64_t p = t * a.K + tid + L::kThreads * q;
-            f.pick[q] = split[p < end ? p : end - 1];
+            const int p = t * a.K + tid + L::kThreads * q;
+            f.pick[q] = split[static_cast<uint32_t>(p < end ? p : end - 1)];
         }
     };
     auto clear = [&]() {
@@ -352,7 +363,7 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
             for (int k = 0; k < 3; ++k)
                 *reinterpret_cast<uint16_t*>(s_stage + old[q] + k * kStageRowBytes) = 0;
     };
-    auto fill_dz = [&](const Stage& f, int64_t t) {
+    auto fill_dz = [&](const Stage& f, int t) {
 #pragma unroll
         for (int q = 0; q < L::Q; ++q) {
             const int i = tid + L::kThreads * q, e = f.pick[q][1] >> 16;
@@ -364,7 +375,7 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
             to[kStageRowBytes] = static_cast<uint16_t>(f.pick[q][1]);
         }
     };
-    auto fill_x = [&](const Stage& f, int64_t t) {
+    auto fill_x = [&](const Stage& f, int t) {
         Pair<BF16> v[L::TPW];
 #pragma unroll
         for (int j = 0; j < L::TPW; ++j) {
@@ -399,36 +410,62 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
     };
 
     f32x16 acc[2][L::TN] = {};
-    auto products = [&]() {
+    struct Operands {
+        bf16x8 z[2][3], x[L::TN][L::XS];
+    };
+    auto read = [&](Operands& f, int ks) {
+        const int ch = ks * 2 + (lane >> 5);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int ch = ks * 2 + (lane >> 5);
-            bf16x8 fz[2][3], fx[L::TN][L::XS];
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
+                f.z[i][k] =
+                    *reinterpret_cast<const bf16x8*>(s_stage + dz_offset(wm * 64 + i * 32 + (lane & 31), k, ch));
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    fz[i][k] = *reinterpret_cast<const bf16x8*>(s_stage +
-                                                                dz_offset(wm * 64 + i * 32 + (lane & 31), k, ch));
+        for (int k = 0; k < L::XS; ++k)
 #pragma unroll
             for (int i = 0; i < L::TN; ++i)
+                f.x[i][k] = *reinterpret_cast<const bf16x8*>(s_stage + L::kX + k * kDwCols * kStageRowBytes +
+                                                             stage_offset(wn * L::NW + i * 32 + (lane & 31), ch));
+    };
+    auto multiply = [&](const Operands& f) {
 #pragma unroll
-                for (int k = 0; k < L::XS; ++k)
-                    fx[i][k] = *reinterpret_cast<const bf16x8*>(
-                        s_stage + L::kX + k * kDwCols * kStageRowBytes +
-                        stage_offset(wn * L::NW + i * 32 + (lane & 31), ch));
+        for (int order = 2; order >= 0; --order)         // small products first
 #pragma unroll
-            for (int order = 2; order >= 0; --order)     // small products first
+            for (int k = 0; k < L::XS; ++k)
+                if (order - k >= 0) {
 #pragma unroll
-                for (int k = 0; k < L::XS; ++k)
-                    if (order - k >= 0) {
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                        for (int j = 0; j < L::TN; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.z[i][order - k], f.x[j][k], acc[i][j],
+                                                                               0, 0, 0);
+                }
+    };
+    auto products = [&]() {
+        if constexpr (L::XS == 1 && L::Q == 1) {
+            // the second half's operands come between the first half's matrix instructions;
+            // with more operands or picks there are not the registers for both
+            constexpr int NR = 6 + L::TN, NM = 2 * L::TN * 3;
+            Operands f[2];
+            __builtin_amdgcn_sched_barrier(0);
+            read(f[0], 0);
+            read(f[1], 1);
+            multiply(f[0]);
+            multiply(f[1]);
+            __builtin_amdgcn_sched_group_barrier(0x100, NR, 0);
+            static_for<0, 2 * NM>([](auto i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if constexpr (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
 #pragma unroll
-                            for (int j = 0; j < L::TN; ++j)
-                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fz[i][order - k], fx[j][k],
-                                                                                   acc[i][j], 0, 0, 0);
-                    }
+            for (int ks = 0; ks < 2; ++ks) {
+                Operands f;
+                read(f, ks);
+                multiply(f);
+            }
         }
     };
 
@@ -440,9 +477,9 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int64_t 
         fill_dz(ahead[0], t0);
     }
     // pairs of stages, the last one perhaps empty
-    for (int64_t t = t0; t < t1; t += 2 * kDwTokens) {
+    for (int t = t0; t < t1; t += 2 * kDwTokens) {
         static_for<0, 2>([&](auto u) {
-            const int64_t tu = t + u * kDwTokens;
+            const int tu = t + u * kDwTokens;
             lds_pipeline_barrier();            // the stage is written
             fetch(ahead[u], tu + 2 * kDwTokens);
             products();
@@ -507,7 +544,7 @@ template <bool BF16, bool EVEN, int ME, int Q>
 static void dw_launch_picks(hipStream_t st, const RouteBackwardArgs& a, int splits, const void* x, const u32x2* split,
                             const uint8_t* alive, float* part, float* dw, float* dbias) {
     using L = DwTile<BF16, ME, Q>;
-    const int64_t per = ((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens;
+    const int per = static_cast<int>(((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens);
     lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16, EVEN, ME, Q>), L::kLds);
     route_dw<BF16, EVEN, ME, Q><<<dim3((a.H + kDwCols) / kDwCols, splits), L::kThreads, L::kLds, st>>>(
         a, per, x, split, alive, part, dw, dbias);
