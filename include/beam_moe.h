@@ -338,8 +338,8 @@ int beam_moe_forward_noalloc(const beam_moe_config* cfg, int64_t T, const void* 
  *              product's gradients -> dispatch_backward -> route_backward
  * They read fewer fields of cfg than the layer (each entry point says which); act_dtype is
  * F32 or BF16 (else BEAM_ERR_UNSUPPORTED), 1 <= topk <= 32, n_experts in [1, 256], any
- * hidden and inter >= 1.  T * topk <= INT32_MAX / 2, and no array holds 2^40 elements or
- * more (BEAM_ERR_INVALID_ARG).  No kernel reads or writes outside the arrays whose sizes
+ * hidden and inter in [1, 2^28].  T * topk <= INT32_MAX / 2, rows <= INT32_MAX, and no
+ * array holds more than 2^40 elements (else BEAM_ERR_INVALID_ARG).  No kernel reads or writes outside the arrays whose sizes
  * the call states, whatever the index arrays hold.
  *
  * Pairs and rows.  Pair p = t * K + i is pick i of token t.  row_of_pair[p] is the row that
@@ -461,7 +461,9 @@ int beam_moe_swiglu_backward(const beam_moe_config* cfg, int64_t T, const void* 
  *   cfg         hidden (at most 2^20), n_experts, topk, routed_scale and act_dtype are read
  *   x           device [T, H] act_dtype, what the router read (FP32 xhat in the sublayer)
  *   w_router    device [H, E] FP32
- *   logits      device [T, E] FP32: the `logits` region of beam_moe_route's workspace
+ *   logits      device [T, E] FP32: the `logits` region of the workspace that
+ *               beam_moe_route (or a forward call) has written, or a copy of it; the next
+ *               call with that workspace overwrites it
  *   ids         device [T, K] int32; an id outside [0, E) is no pick: it enters no sum (for
  *               padding tokens; to leave out single picks, pass zero gradients for them)
  *   dweights    device [T, K] FP32

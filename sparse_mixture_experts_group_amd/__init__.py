@@ -402,7 +402,7 @@ def _rows_by(t, name):
 
 def route_logits(cfg, T, ws):
     """The logits [T, E] that the last beam_moe_route or forward call left in its workspace
-    (a view; beam_moe_route_backward reads them)."""
+    (a view, which beam_moe_route_backward reads; the next call with ws overwrites it)."""
     import torch
     at = beam_moe_workspace_map(cfg, T)["logits"]
     return ws[at:at + 4 * T * cfg.n_experts].view(torch.float32).view(T, cfg.n_experts)

@@ -18,13 +18,15 @@ bool optional(const void* p) { return !p || aligned16(p); }
 
 // Elements of one array: grids are counted in 32 bits, 8 elements a thread.
 constexpr int64_t kMaxElements = int64_t{1} << 40;
+// Columns of a row: kernels count them in 32 bits, with a block's stride beyond the end.
+constexpr int64_t kMaxWidth = int64_t{1} << 28;
 
 // Tokens, picks and (width >= 0) a row width that an operator takes.
 int check_pairs(const beam_moe_config* c, int64_t T, int64_t width) {
     if (!c || T < 0) return BEAM_ERR_INVALID_ARG;
     if (c->topk < 1 || c->topk > kMaxTopK) return BEAM_ERR_INVALID_ARG;
     if (T > INT32_MAX / 2 / c->topk) return BEAM_ERR_INVALID_ARG;
-    if (width < 1) return BEAM_ERR_INVALID_ARG;
+    if (width < 1 || width > kMaxWidth) return BEAM_ERR_INVALID_ARG;
     if (T > 0 && width > kMaxElements / T / c->topk) return BEAM_ERR_INVALID_ARG;
     return BEAM_OK;
 }
@@ -141,8 +143,7 @@ int beam_moe_combine_backward(const beam_moe_config* cfg, int64_t T, const void*
 static int check_swiglu(const beam_moe_config* cfg, int64_t T, const int32_t* row_of_pair, int64_t rows) {
     int s = check_pairs(cfg, T, cfg ? cfg->inter : 0);
     if (s != BEAM_OK) return s;
-    if (rows < 0 || rows > INT32_MAX || cfg->inter > INT32_MAX / 2 || rows > kMaxElements / cfg->inter)
-        return BEAM_ERR_INVALID_ARG;
+    if (rows < 0 || rows > INT32_MAX || rows > kMaxElements / cfg->inter) return BEAM_ERR_INVALID_ARG;
     if (T > 0 && !row_of_pair && cfg->topk != 1) return BEAM_ERR_INVALID_ARG;
     return check_act(cfg);
 }

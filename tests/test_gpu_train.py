@@ -412,6 +412,62 @@ def test_swiglu_dense(T, I, dt, source8):
     swiglu_check(dt, I, 1, None, None, rand(1, T, 2 * I, dt=dt, scale=3.0), None, rand(2, T, I, dt=dt), source8)
 
 
+@pytest.mark.parametrize("T", [33, 1100])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_swiglu_of_mapped_rows_without_weights(T, dt):
+    """Weights applied elsewhere: ones here and no gradient of them; in the order of pairs and
+    (from 8192 pairs) of rows, which have to agree bit for bit with weights of one."""
+    K, I = 8, 72
+    row, pair, row_d = routed(T, T, 9, K, 0.2)
+    cfg = config(dt, I=I, E=9, K=K)
+    gu, dh = rand(1, T * K, 2 * I, dt=dt).cuda(), rand(2, T * K, I, dt=dt).cuda()
+    ones = torch.ones(T, K, device="cuda")
+    h = lambda: torch.full((T * K, I), -3.0, dtype=TORCH[dt], device="cuda")
+    d = lambda: torch.full((T * K, 2 * I), -3.0, dtype=TORCH[dt], device="cuda")
+    a = bm.beam_moe_swiglu(cfg, gu, row_of_pair=row_d, h=h())
+    assert torch.equal(a, bm.beam_moe_swiglu(cfg, gu, weights=ones, row_of_pair=row_d, h=h()))
+    assert (a[torch.from_numpy(pair < 0).cuda()] == -3.0).all()
+    dgu, again, none = bm.beam_moe_swiglu_backward(cfg, dh, gu, row_of_pair=row_d, dgu=d(), h=h())
+    dgu1, again1, dw = bm.beam_moe_swiglu_backward(cfg, dh, gu, weights=ones, row_of_pair=row_d, dgu=d(), h=h())
+    assert none is None and torch.equal(dgu, dgu1) and torch.equal(again, again1) and torch.equal(again, a)
+    # a buffer of more rows than pairs, and the weights without their gradient (C entry)
+    import ctypes
+    big = torch.full((T * K + 70, I), -3.0, dtype=TORCH[dt], device="cuda")
+    gu2 = torch.cat([gu, torch.full((70, 2 * I), float("nan"), dtype=TORCH[dt], device="cuda")])
+    bm.beam_moe_swiglu(cfg, gu2, weights=ones, row_of_pair=row_d, h=big)
+    assert torch.equal(big[:T * K], a) and (big[T * K:] == -3.0).all()
+    ws = torch.full((bm.beam_moe_swiglu_workspace_size(cfg, T, T * K) + 16,), 255, dtype=torch.uint8, device="cuda")
+    out = d()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    st = bm.lib().beam_moe_swiglu_backward(ctypes.byref(cfg), T, p(dh), p(gu), None, p(row_d), T * K, p(ones), p(out), None,
+                                           None, p(ws), ws.numel(),
+                                           ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == bm.BEAM_OK and torch.equal(out, dgu)
+
+
+def test_swiglu_offsets_past_32_bits():
+    """gu with more than 2^31 elements, rows in order: the last rows are right."""
+    T, K, I = 33000, 8, 4104
+    cfg = config("bf16", I=I, E=8, K=K)
+    ids = torch.arange(8, dtype=torch.int32, device="cuda").repeat(T, 1)
+    _, row, pair = bm.beam_moe_sort(cfg, ids)
+    gu = torch.randn(4000, 2 * I, device="cuda").to(torch.bfloat16).repeat(66, 1)
+    assert gu.numel() > 2 ** 31 and gu.shape[0] == T * K
+    w = torch.rand(T, K, device="cuda")
+    h, q, scale = bm.beam_moe_swiglu(cfg, gu, weights=w, row_of_pair=row, keep8=True)
+    dh = h.clone()
+    dgu, again, dw = bm.beam_moe_swiglu_backward(cfg, dh, q, gu_scale=scale, weights=w, row_of_pair=row)
+    for lo in (0, T * K - 300):
+        part = slice(lo, lo + 300)
+        one = config("bf16", I=I, E=8, K=1)
+        wr = w.reshape(-1)[pair[part].long()].reshape(-1, 1).contiguous()
+        h1, q1, s1 = bm.beam_moe_swiglu(one, gu[part].contiguous(), weights=wr, keep8=True)
+        d1, a1, w1 = bm.beam_moe_swiglu_backward(one, dh[part].contiguous(), q1, gu_scale=s1, weights=wr)
+        assert torch.equal(h[part], h1) and torch.equal(scale[part], s1) and torch.equal(dgu[part], d1)
+        assert torch.equal(q[part].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(again[part], a1)
+        assert torch.equal(dw.reshape(-1)[pair[part].long()], w1.reshape(-1))
+
+
 def test_swiglu_far_arguments():
     """Gates far out: sigma saturates without NaN, gradients go to their limits."""
     g = torch.tensor([0.0, -0.0, 1e-30, 30.0, 88.0, 200.0, 1e30, -30.0, -87.0, -88.5, -104.0, -200.0, -1e30, 1.2785, -1.2785,

@@ -66,8 +66,9 @@ def test_bad_configs_and_counts(call):
         assert call(c) == ARG
         assert call(cfg(act_dtype=9)) == ARG
         assert call(cfg(act_dtype=bm.BEAM_DTYPE_FP8_E4M3)) == UNSUPPORTED
-        wide = cfg(hidden=1 << 30, inter=1 << 29)
-        assert call(wide, T=1 << 20) == ARG                # an array of 2^50 elements
+        assert call(cfg(hidden=1 << 28, inter=1 << 28), T=1 << 20) == ARG      # an array of 2^48 elements
+        assert call(cfg(hidden=(1 << 28) + 1, inter=(1 << 28) + 1)) == ARG
+        assert call(cfg(hidden=2 ** 31 - 1, inter=2 ** 31 - 1), T=1) == ARG
     fn = getattr(bm.lib(), "beam_moe_" + call.__name__)
     args = [0 if t is not ctypes.c_void_p else None for t in fn.argtypes[2:]]
     assert fn(None, 4, *args) == ARG                       # no configuration
