@@ -427,8 +427,8 @@ int beam_moe_combine_backward(const beam_moe_config* cfg, int64_t T, const void*
  *   keep_q      device [rows, 2I] bytes out, keep_scale device [rows, 2, ceil(I/32)] bytes
  *               out: the 8-bit copy of gu, each half blocked on its own; both or neither
  *   ws          device workspace of ws_bytes >= beam_moe_swiglu_workspace_size(cfg, T, rows):
- *               4 bytes a row from 8192 pairs on, 0 for less (NULL is accepted then, and with
- *               row_of_pair NULL)
+ *               4 bytes a row where T * topk * inter >= 2^24, 0 for less (NULL is accepted
+ *               then, and with row_of_pair NULL)
  */
 size_t beam_moe_swiglu_workspace_size(const beam_moe_config* cfg, int64_t T, int64_t rows);
 

@@ -156,11 +156,11 @@ static SwigluArgs swiglu_args(const beam_moe_config* c, int64_t T, int64_t rows,
 
 // Workspace of a SwiGLU call that takes rows in order.
 static size_t swiglu_ws(const beam_moe_config* c, int64_t T, int64_t rows) {
-    return T * c->topk >= kRowOrderPairs ? sizeof(int32_t) * static_cast<size_t>(rows) : 0;
+    return T * c->topk * c->inter >= kRowOrderValues ? sizeof(int32_t) * static_cast<size_t>(rows) : 0;
 }
 
 size_t beam_moe_swiglu_workspace_size(const beam_moe_config* cfg, int64_t T, int64_t rows) {
-    if (check_pairs(cfg, T, 1) != BEAM_OK || rows < 0 || rows > INT32_MAX) return 0;
+    if (check_pairs(cfg, T, cfg ? cfg->inter : 0) != BEAM_OK || rows < 0 || rows > INT32_MAX) return 0;
     return swiglu_ws(cfg, T, rows);
 }
 

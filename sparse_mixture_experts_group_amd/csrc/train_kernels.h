@@ -27,9 +27,12 @@ void launch_sort_pairs(hipStream_t st, int64_t pairs, int E, const int32_t* ids,
                        int32_t* row_of_pair, int32_t* pair_of_row, int32_t* counts);
 
 // ---- rows (dispatch.hip) --------------------------------------------------
-// Pairs from which the SwiGLU operators take rows in order; they need a workspace of an
-// int32 a row then.
-constexpr int64_t kRowOrderPairs = 8192;
+// Values of h from which the SwiGLU operators take rows in order; they need a workspace of
+// an int32 a row then.  Forward and backward from the 8-bit copy, in the order of pairs
+// against that of rows: 16384 pairs of 512 columns 14.9 and 18.8 us against 16.8 and 20.2,
+// 32768 of 512 27.9 and 34.9 against 27.8 and 33.3, 8192 of 2560 34.8 and 44.1 against 33.3
+// and 42.3, 65536 of 2560 266 and 337 against 233 and 303.
+constexpr int64_t kRowOrderValues = int64_t{1} << 24;
 
 // pair_of_row [rows] from row_of_pair [pairs]; a dropped pair's dweights (if given) are zeros.
 void launch_invert(hipStream_t st, int64_t pairs, int64_t rows, const int32_t* row_of_pair, int32_t* pair_of_row,

@@ -124,7 +124,7 @@ SHAPES = [  # T, H, E, K, drop
     (1, 1, 1, 1, 0), (1, 5120, 256, 8, 0), (5, 7, 3, 2, 0.3), (17, 32, 256, 8, 0.3), (33, 33, 60, 9, 0.2),
     (9, 64, 4, 4, 0), (40, 257, 16, 6, 0.3), (130, 520, 32, 32, 0.1), (64, 1001, 7, 3, 0), (300, 1000, 256, 8, 0.2),
     (2100, 96, 12, 2, 0.3), (3, 12000, 8, 5, 0.3), (2049, 640, 9, 1, 0),
-    (1024, 40, 60, 8, 0.3), (1023, 33, 7, 8, 0), (2800, 1032, 9, 3, 0.3)]     # 8192 pairs and more: rows in order
+    (1024, 40, 60, 8, 0.3), (1023, 33, 7, 8, 0), (2800, 1032, 9, 3, 0.3)]
 
 
 def routed(seed, T, E, K, drop):
@@ -310,7 +310,7 @@ def test_keep_borders():
 SWIGLU = [  # T, I, E, K, drop
     (1, 1, 1, 1, 0), (16, 2560, 256, 8, 0), (5, 7, 3, 2, 0.3), (17, 32, 16, 8, 0.3), (33, 33, 60, 9, 0.2),
     (40, 257, 16, 6, 0.3), (64, 1001, 7, 3, 0), (300, 504, 256, 8, 0.2), (700, 96, 12, 3, 0.3), (3, 20480, 8, 2, 0.3),
-    (1024, 40, 60, 8, 0.2), (1023, 33, 7, 8, 0), (2800, 520, 9, 3, 0.3)]      # 8192 pairs and more: rows in order
+    (1024, 40, 60, 8, 0.2), (1023, 33, 7, 8, 0)]
 
 
 def swiglu_ref(gu, w, I):
@@ -412,12 +412,56 @@ def test_swiglu_dense(T, I, dt, source8):
     swiglu_check(dt, I, 1, None, None, rand(1, T, 2 * I, dt=dt, scale=3.0), None, rand(2, T, I, dt=dt), source8)
 
 
-@pytest.mark.parametrize("T", [33, 1100])
+@pytest.mark.parametrize("source8", [False, True])
+@pytest.mark.parametrize("T,K,I,drop", [(1024, 8, 2048, 0.2), (700, 6, 4001, 0.0), (9000, 1, 1866, 0.5), (17, 8, 130000, 0.3)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_swiglu_of_mapped_rows_without_weights(T, dt):
+def test_swiglu_rows_in_order(T, K, I, drop, dt, source8):
+    """From 2^24 values on the rows are taken in order: bit for bit what the call without a map
+    (checked against the formulas) gives for the same rows, rows of no pair left alone, zeros
+    for the weights of dropped pairs; in place too."""
+    row, pair, row_d = routed(T, T, 9, K, drop)
+    R = T * K + 5                                          # rows behind the last pair
+    cfg, one = config(dt, I=I, E=9, K=K), config(dt, I=I, E=9, K=1)
+    assert bm.beam_moe_swiglu_workspace_size(cfg, T, R) >= 4 * R
+    g = torch.Generator("cuda").manual_seed(T)
+    gu = (3 * torch.randn(R, 2 * I, generator=g, device="cuda")).to(TORCH[dt])
+    dh = torch.randn(R, I, generator=g, device="cuda").to(TORCH[dt])
+    w = torch.rand(T, K, generator=g, device="cuda") + 0.5
+    live = torch.zeros(R, dtype=torch.bool, device="cuda")
+    live[:T * K] = torch.from_numpy(pair >= 0)
+    wr = torch.ones(R, 1, device="cuda")
+    wr[:T * K, 0] = w.reshape(-1)[torch.from_numpy(np.maximum(pair, 0)).long().cuda()]
+    gu[~live] = float("nan")
+    full = lambda n, v, t=TORCH[dt]: torch.full((R, n), v, dtype=t, device="cuda")
+    scale0 = torch.full((R, 2, bm.keep_blocks(I)), 9, dtype=torch.uint8, device="cuda")
+    h, q, scale = bm.beam_moe_swiglu(cfg, gu, weights=w, row_of_pair=row_d, h=full(I, -3.0),
+                                     keep_q=full(2 * I, 9, torch.uint8), keep_scale=scale0.clone())
+    h1, q1, scale1 = bm.beam_moe_swiglu(one, gu, weights=wr, keep8=True)
+    keep = lambda a, b, still: torch.where(live.view(-1, *[1] * (a.dim() - 1)), b, torch.full_like(b, still))
+    assert torch.equal(h, keep(h, h1, -3.0)) and torch.equal(scale, keep(scale, scale1, 9))
+    assert torch.equal(q, keep(q, q1.view(torch.uint8), 9))
+    src, src_scale = (q, scale) if source8 else (gu, None)
+    src1, src1_scale = (q1, scale1) if source8 else (gu, None)
+    dgu, again, dw = bm.beam_moe_swiglu_backward(cfg, dh, src, gu_scale=src_scale, weights=w, row_of_pair=row_d,
+                                                 dgu=full(2 * I, -3.0), h=full(I, -3.0))
+    dgu1, again1, dw1 = bm.beam_moe_swiglu_backward(one, dh, src1, gu_scale=src1_scale, weights=wr)
+    assert torch.equal(dgu, keep(dgu, dgu1, -3.0)) and torch.equal(again, keep(again, again1, -3.0))
+    want = torch.zeros(T * K, device="cuda")
+    want[torch.from_numpy(pair[pair >= 0]).long().cuda()] = dw1[:T * K, 0][live[:T * K]]
+    assert torch.equal(dw.reshape(-1), want)
+    if not source8:
+        over, dover = gu.clone(), dh.clone()
+        bm.beam_moe_swiglu_backward(cfg, dover, over, weights=w, row_of_pair=row_d, dgu=over, h=dover)
+        assert torch.equal(over[live], dgu[live]) and torch.equal(dover[live], again[live])
+        assert torch.equal(dover[~live], dh[~live])
+
+
+@pytest.mark.parametrize("T,I", [(33, 72), (1100, 2000)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_swiglu_of_mapped_rows_without_weights(T, I, dt):
     """Weights applied elsewhere: ones here and no gradient of them; in the order of pairs and
-    (from 8192 pairs) of rows, which have to agree bit for bit with weights of one."""
-    K, I = 8, 72
+    (from 2^24 values) of rows, which have to agree bit for bit with weights of one."""
+    K = 8
     row, pair, row_d = routed(T, T, 9, K, 0.2)
     cfg = config(dt, I=I, E=9, K=K)
     gu, dh = rand(1, T * K, 2 * I, dt=dt).cuda(), rand(2, T * K, I, dt=dt).cuda()
@@ -696,12 +740,12 @@ def step_buffers(seed, T, H, I, E, K):
     return {k: v.cuda() for k, v in b.items()}
 
 
-@pytest.mark.parametrize("T", [24, 1400])
-def test_captured_step_replays(T):
+@pytest.mark.parametrize("T,I", [(24, 136), (1400, 136), (1400, 1504)])      # the last: SwiGLU rows in order
+def test_captured_step_replays(T, I):
     """Every replay, with other eager work between them, equals the eager calls on the
     buffers' contents of that time."""
-    shape = (T, 264, 136, 20, 8)
-    cfg = config("bf16", H=264, I=136, E=20, K=8)
+    shape = (T, 264, I, 20, 8)
+    cfg = config("bf16", H=264, I=I, E=20, K=8)
     b = step_buffers(1, *shape)
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):

@@ -137,13 +137,14 @@ def test_swiglu_arguments():
 
 
 def test_swiglu_workspace():
-    T = 8192 // 3 + 1                                      # from here on rows are taken in order
-    need = bm.beam_moe_swiglu_workspace_size(cfg(), T, 100)
-    assert need >= 400 and bm.beam_moe_swiglu_workspace_size(cfg(), T - 1, 100) == 0
+    c, T = cfg(inter=1 << 12), 4096 // 3 + 1               # from 2^24 values on rows are taken in order
+    need = bm.beam_moe_swiglu_workspace_size(c, T, 100)
+    assert need >= 400 and bm.beam_moe_swiglu_workspace_size(c, T - 1, 100) == 0
     assert bm.beam_moe_swiglu_workspace_size(cfg(topk=0), T, 100) == 0
+    assert bm.beam_moe_swiglu_workspace_size(cfg(inter=0), T, 100) == 0
     for call in (swiglu, swiglu_backward):
-        assert call(T=T, rows=100) == WS and call(T=T, rows=100, ws=P, nb=need - 1) == WS
-        assert call(T=T, rows=100, ws=ODD, nb=need) == ARG
+        assert call(c, T=T, rows=100) == WS and call(c, T=T, rows=100, ws=P, nb=need - 1) == WS
+        assert call(c, T=T, rows=100, ws=ODD, nb=need) == ARG
 
 
 def test_route_backward_arguments():
