@@ -162,7 +162,10 @@ __device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
 // walks its tokens: K reads of 512 bytes a token instead of a dense product over E.  A row
 // of 16 lanes takes a token, 8 columns a lane, and holds the token's picks, a pick a lane
 // (two for K > 16), which its lanes take from each other inside the vector instructions.
-// The picks and addends of a wave's next tokens are loaded before it works on these.
+// The picks and addends of a wave's next tokens are loaded before it works on these.  Bound
+// by HBM: 32768 tokens of 5120 BF16 columns with addends 135 us, 5.0 TB/s, 8192 in FP32 75
+// us, a tenth of it W's way into LDS.  (A wave a token, two columns a lane, picks by scalar
+// register: 222 us, bound by its vector instructions.)
 // ---------------------------------------------------------------------------
 constexpr int kDxStep = 2;         // tokens of a row of lanes in flight
 
@@ -276,10 +279,10 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
 // after the products.  One buffer: two blocks share a CU (57 KB each for 256 experts and
 // BF16), and one's products run while the other writes its stage.  A stage's values are
 // loaded into registers a stage ahead.  Token ranges (blockIdx.y) write partial sums
-// [H+1, E], a single range the gradients themselves.  Matrix-bound: the three (FP32: six)
-// products of 32768 tokens (8192) run at 1.35 PFLOP/s, where a large library product in
-// BF16 reaches 1.24; the same sums as FP32 additions in LDS, a lane a column, took 9.7 ms
-// where this takes 0.2.
+// [H+1, E], a single range the gradients themselves.  Matrix-bound: 32768 tokens of 5120
+// columns in BF16 take 0.21 ms, 1.2 PFLOP/s of the three products, 8192 in FP32 0.115 ms,
+// 1.1 of the six; a large library product in BF16 reaches 1.24.  The same sums as FP32
+// additions in LDS, a lane a column, took 9.8 and 2.2 ms.
 template <bool BF16, int ME, int Q_>
 struct DwTile {
     static constexpr int W = 4, kThreads = W * 64;       // waves, threads

@@ -25,7 +25,8 @@ __device__ __forceinline__ float sigmoid_fast(float g) { return __builtin_amdgcn
 
 // ---------------------------------------------------------------------------
 // h[r] = w g sigma(g) u, (g, u) the halves of gu[r].  A thread has 8 columns of g and the
-// same of u.
+// same of u, four lanes a block of the 8-bit copy.  Bound by HBM: 65536 mapped rows of 2560
+// BF16 columns with the copy 227 us (6.0 TB/s; a plain copy reaches 6.65).
 // ---------------------------------------------------------------------------
 template <bool BF16, bool ALIGNED, bool KEEP>
 __global__ __launch_bounds__(256) void swiglu_rows(SwigluArgs a, int pieces, const void* __restrict__ gu,
@@ -92,7 +93,8 @@ void launch_swiglu(hipStream_t st, const SwigluArgs& a, const void* gu, void* h,
 //   dg = w dh u s (1 + g (1 - s)),  du = w dh a,  h = w a u (again, for the down weights'
 //   gradient),  dw = sum over the row of dh a u.
 // A thread reads its columns before it writes them, so dgu may lie over an FP32 or BF16 gu,
-// and h over dh.
+// and h over dh.  Bound by HBM: from the 8-bit copy, 65536 mapped rows of 2560 BF16 columns
+// with dw 300 us (5.6 TB/s), 4096 rows of 20480 without 133 us (6.3).
 // ---------------------------------------------------------------------------
 // One 8-column piece of a row: its values,
 template <bool BF16, bool ALIGNED, bool SRC8>
