@@ -328,10 +328,9 @@ void launch_combine_rows(hipStream_t st, const RowArgs& a, const void* in, void*
 // streams as experts: 8192 tokens of 5120 BF16 columns 268 us (5.3 TB/s).  In the order of
 // rows (one stream each, as the SwiGLU) dy is read K times over: 365 us.
 // ---------------------------------------------------------------------------
-template <bool BF16, bool ALIGNED, bool DOT>
+template <bool BF16, bool ALIGNED, bool DOT, int P>
 __global__ __launch_bounds__(1024) void combine_backward(RowArgs a, int group, const void* __restrict__ dy,
                                                          const void* eo, void* deo, float* __restrict__ dweights) {
-    constexpr int P = BF16 ? 8 : 4;            // picks at a time (32 registers of eo)
     __shared__ float s_dot[P][16];
     const int lane = group <= 64 ? threadIdx.x & (group - 1) : threadIdx.x;
     const int64_t t = group <= 64 ? static_cast<int64_t>(blockIdx.x) * (256 / group) + threadIdx.x / group : blockIdx.x;
@@ -402,13 +401,27 @@ __global__ __launch_bounds__(1024) void combine_backward(RowArgs a, int group, c
     }
 }
 
-template <bool BF16, bool ALIGNED>
-static void combine_backward_typed(hipStream_t st, const RowArgs& a, int group, const void* dy, const void* eo,
+template <bool BF16, bool ALIGNED, int P>
+static void combine_backward_picks(hipStream_t st, const RowArgs& a, int group, const void* dy, const void* eo,
                                    void* deo, float* dweights) {
     const unsigned blocks = group_blocks(a.T, group);
     const int threads = group_threads(group);
-    if (eo) combine_backward<BF16, ALIGNED, true><<<blocks, threads, 0, st>>>(a, group, dy, eo, deo, dweights);
-    else combine_backward<BF16, ALIGNED, false><<<blocks, threads, 0, st>>>(a, group, dy, nullptr, deo, nullptr);
+    if (eo) combine_backward<BF16, ALIGNED, true, P><<<blocks, threads, 0, st>>>(a, group, dy, eo, deo, dweights);
+    else combine_backward<BF16, ALIGNED, false, P><<<blocks, threads, 0, st>>>(a, group, dy, nullptr, deo, nullptr);
+}
+
+// P picks at a time, 32 registers of eo at most.  Of BF16 fewer where there are fewer picks:
+// the waves then need half the registers, and twice as many are there to wait for memory.
+// 4096 tokens of 5120 BF16 columns: two picks 36 us at two at a time, 45 at eight; four 68
+// at four, 71 at eight.  FP32 stays at four: two picks 78 us, at two at a time 82.
+template <bool BF16, bool ALIGNED>
+static void combine_backward_typed(hipStream_t st, const RowArgs& a, int group, const void* dy, const void* eo,
+                                   void* deo, float* dweights) {
+    if constexpr (BF16) {
+        if (a.K <= 2) return combine_backward_picks<BF16, ALIGNED, 2>(st, a, group, dy, eo, deo, dweights);
+        if (a.K > 4) return combine_backward_picks<BF16, ALIGNED, 8>(st, a, group, dy, eo, deo, dweights);
+    }
+    combine_backward_picks<BF16, ALIGNED, 4>(st, a, group, dy, eo, deo, dweights);
 }
 
 void launch_combine_backward(hipStream_t st, const RowArgs& a, const void* dy, const void* eo, void* deo,

@@ -124,7 +124,8 @@ SHAPES = [  # T, H, E, K, drop
     (1, 1, 1, 1, 0), (1, 5120, 256, 8, 0), (5, 7, 3, 2, 0.3), (17, 32, 256, 8, 0.3), (33, 33, 60, 9, 0.2),
     (9, 64, 4, 4, 0), (40, 257, 16, 6, 0.3), (130, 520, 32, 32, 0.1), (64, 1001, 7, 3, 0), (300, 1000, 256, 8, 0.2),
     (2100, 96, 12, 2, 0.3), (3, 12000, 8, 5, 0.3), (2049, 640, 9, 1, 0),
-    (1024, 40, 60, 8, 0.3), (1023, 33, 7, 8, 0), (2800, 1032, 9, 3, 0.3)]
+    (1024, 40, 60, 8, 0.3), (1023, 33, 7, 8, 0), (2800, 1032, 9, 3, 0.3),
+    (1900, 2048, 12, 2, 0.3), (700, 2051, 8, 4, 0.3)]
 
 
 def routed(seed, T, E, K, drop):
