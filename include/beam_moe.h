@@ -338,9 +338,12 @@ int beam_moe_forward_noalloc(const beam_moe_config* cfg, int64_t T, const void* 
  *              product's gradients -> dispatch_backward -> route_backward
  * They read fewer fields of cfg than the layer (each entry point says which); act_dtype is
  * F32 or BF16 (else BEAM_ERR_UNSUPPORTED), 1 <= topk <= 32, n_experts in [1, 256], any
- * hidden and inter in [1, 2^28].  T * topk <= INT32_MAX / 2, rows <= INT32_MAX, and no
- * array holds more than 2^40 elements (else BEAM_ERR_INVALID_ARG).  No kernel reads or writes outside the arrays whose sizes
- * the call states, whatever the index arrays hold.
+ * hidden and inter in [1, 2^28].  T * topk <= INT32_MAX / 2, rows <= INT32_MAX, no array
+ * holds more than 2^40 elements, and a launch has fewer than 2^32 threads of 8 columns (else
+ * BEAM_ERR_INVALID_ARG): the rows that an operator goes over (dispatch and combine T, swiglu
+ * the larger of T * topk and rows) times the width, counted up to a multiple of 64 columns,
+ * may always be up to 2^34.  No kernel reads or writes outside the arrays whose sizes the
+ * call states, whatever the index arrays hold.
  *
  * Pairs and rows.  Pair p = t * K + i is pick i of token t.  row_of_pair[p] is the row that
  * holds it in a buffer of `rows` rows; a value outside [0, rows) means that the pair is
@@ -427,8 +430,8 @@ int beam_moe_combine_backward(const beam_moe_config* cfg, int64_t T, const void*
  *   keep_q      device [rows, 2I] bytes out, keep_scale device [rows, 2, ceil(I/32)] bytes
  *               out: the 8-bit copy of gu, each half blocked on its own; both or neither
  *   ws          device workspace of ws_bytes >= beam_moe_swiglu_workspace_size(cfg, T, rows):
- *               4 bytes a row where T * topk * inter >= 2^24, 0 for less (NULL is accepted
- *               then, and with row_of_pair NULL)
+ *               4 bytes a row where T * topk * inter >= 2^24 and rows <= 5/4 T * topk, else
+ *               0 (NULL is accepted then, and with row_of_pair NULL)
  */
 size_t beam_moe_swiglu_workspace_size(const beam_moe_config* cfg, int64_t T, int64_t rows);
 

@@ -165,7 +165,7 @@ void launch_sort_pairs(hipStream_t st, int64_t pairs, int E, const int32_t* ids,
 }
 
 // pair_of_row for operators that take rows in order: one stream of addresses an array,
-// instead of one an expert, is worth this pass of 8 bytes a pair from kRowOrderValues on.
+// instead of one an expert, is worth this pass of 8 bytes a pair where rows_in_order says so.
 __global__ __launch_bounds__(256) void invert_rows(int64_t pairs, int64_t rows, const int32_t* __restrict__ row_of_pair,
                                                    int32_t* __restrict__ pair_of_row, float* __restrict__ dweights) {
     const int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;

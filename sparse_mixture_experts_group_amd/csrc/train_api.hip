@@ -5,6 +5,7 @@
 #include "beam_moe.h"
 #include "kernels.h"
 #include "train_kernels.h"
+#include "train_rows.cuh"
 
 using namespace beam;
 
@@ -16,8 +17,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool given(const void* p) { return p && aligned16(p); }
 bool optional(const void* p) { return !p || aligned16(p); }
 
-// Elements of one array: grids are counted in 32 bits, 8 elements a thread.
+// Elements of one array: their offsets in bytes stay far from 64 bits.
 constexpr int64_t kMaxElements = int64_t{1} << 40;
+// Threads of one launch: a grid's are counted in 32 bits, and fill whole blocks.
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1024;
 // Columns of a row: kernels count them in 32 bits, with a block's stride beyond the end.
 constexpr int64_t kMaxWidth = int64_t{1} << 28;
 
@@ -40,6 +43,7 @@ int check_rows_call(const beam_moe_config* c, int64_t T, int64_t rows) {
     int s = check_pairs(c, T, c ? c->hidden : 0);
     if (s != BEAM_OK) return s;
     if (rows < 0 || rows > INT32_MAX || rows > kMaxElements / c->hidden) return BEAM_ERR_INVALID_ARG;
+    if (T > kMaxThreads / row_threads(c->hidden)) return BEAM_ERR_INVALID_ARG;
     return check_act(c);
 }
 
@@ -144,6 +148,8 @@ static int check_swiglu(const beam_moe_config* cfg, int64_t T, const int32_t* ro
     int s = check_pairs(cfg, T, cfg ? cfg->inter : 0);
     if (s != BEAM_OK) return s;
     if (rows < 0 || rows > INT32_MAX || rows > kMaxElements / cfg->inter) return BEAM_ERR_INVALID_ARG;
+    const int64_t pairs = T * cfg->topk, items = rows_in_order(pairs, rows, cfg->inter) && rows > pairs ? rows : pairs;
+    if (items > kMaxThreads / row_threads(cfg->inter)) return BEAM_ERR_INVALID_ARG;
     if (T > 0 && !row_of_pair && cfg->topk != 1) return BEAM_ERR_INVALID_ARG;
     return check_act(cfg);
 }
@@ -156,7 +162,7 @@ static SwigluArgs swiglu_args(const beam_moe_config* c, int64_t T, int64_t rows,
 
 // Workspace of a SwiGLU call that takes rows in order.
 static size_t swiglu_ws(const beam_moe_config* c, int64_t T, int64_t rows) {
-    return T * c->topk * c->inter >= kRowOrderValues ? sizeof(int32_t) * static_cast<size_t>(rows) : 0;
+    return rows_in_order(T * c->topk, rows, c->inter) ? sizeof(int32_t) * static_cast<size_t>(rows) : 0;
 }
 
 size_t beam_moe_swiglu_workspace_size(const beam_moe_config* cfg, int64_t T, int64_t rows) {

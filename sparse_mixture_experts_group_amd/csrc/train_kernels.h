@@ -33,6 +33,15 @@ void launch_sort_pairs(hipStream_t st, int64_t pairs, int E, const int32_t* ids,
 // 32768 of 512 27.9 and 34.9 against 27.8 and 33.3, 8192 of 2560 34.8 and 44.1 against 33.3
 // and 42.3, 65536 of 2560 266 and 337 against 233 and 303.
 constexpr int64_t kRowOrderValues = int64_t{1} << 24;
+// Rows in order are read whether they have a pair or not: not where more than a quarter of
+// a buffer is room to spare.  65536 pairs of 2560 columns, forward and backward, pairs
+// against rows: 1.15 rows a pair 261 and 331 us against 244 and 322, 1.25 257 and 326
+// against 256 and 332, 1.5 254 and 328 against 278 and 354, 2 256 and 325 against 330 and
+// 404.  With half as many rows as pairs (the rest on other devices) 148 and 217 against 132
+// and 173.
+inline bool rows_in_order(int64_t pairs, int64_t rows, int64_t cols) {
+    return pairs * cols >= kRowOrderValues && rows * 4 <= pairs * 5;
+}
 
 // pair_of_row [rows] from row_of_pair [pairs]; a dropped pair's dweights (if given) are zeros.
 void launch_invert(hipStream_t st, int64_t pairs, int64_t rows, const int32_t* row_of_pair, int32_t* pair_of_row,
@@ -66,7 +75,6 @@ struct SwigluArgs {
     const float* weights;        // [pairs] or null (ones)
     int32_t* pair_of_row;        // [rows] of workspace: rows are taken in order; or null: pairs are
 };
-
 
 void launch_swiglu(hipStream_t st, const SwigluArgs& a, const void* gu, void* h, uint8_t* keep_q, uint8_t* keep_scale);
 // gu_scale: gu holds E4M3 codes.  h and dweights may be null.

@@ -279,6 +279,13 @@ inline int row_group(int cols, int most) {
     return g;
 }
 
+// Threads that an operator has for one row, at most: a group, or the packed pieces (of whole
+// blocks of the 8-bit copy).
+inline int64_t row_threads(int cols) {
+    const int pieces = (cols + 31) / 32 * 4, group = row_group(cols, 1024);
+    return pieces > group ? pieces : group;
+}
+
 // Threads of a block, and blocks, for `rows` rows of such a group.
 inline int group_threads(int group) { return group <= 64 ? 256 : group; }
 inline unsigned group_blocks(int64_t rows, int group) {

@@ -490,6 +490,45 @@ def test_swiglu_of_mapped_rows_without_weights(T, I, dt):
     assert st == bm.BEAM_OK and torch.equal(out, dgu)
 
 
+@pytest.mark.parametrize("source8", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_swiglu_rows_to_spare(dt, source8):
+    """A buffer with room behind each expert's rows (a capacity), of as many values as are
+    taken in the order of rows without it: bit for bit the compact buffer's results, the room
+    left alone."""
+    T, K, I, E, cap = 1024, 8, 2048, 9, 2600
+    off, row, pair = sorted_rows(picks(5, T, E, K, 0.2), E)
+    cfg, row_d, live = config(dt, I=I, E=E, K=K), torch.from_numpy(row).cuda(), int(off[E])
+    assert T * K * I >= 2 ** 24 and E * cap > 2 * T * K and np.diff(off).max() < cap
+    expert = np.repeat(np.arange(E), np.diff(off))
+    place = torch.from_numpy(np.arange(live) - off[expert] + expert * cap).cuda()     # compact row -> its place
+    far = torch.where(row_d >= 0, place[row_d.long().clamp(min=0)], -1).int()
+    g = torch.Generator("cuda").manual_seed(3)
+    gu = (3 * torch.randn(live, 2 * I, generator=g, device="cuda")).to(TORCH[dt])
+    dh = torch.randn(live, I, generator=g, device="cuda").to(TORCH[dt])
+    w = torch.rand(T, K, generator=g, device="cuda") + 0.5
+
+    def spread(t, room):
+        out = torch.full((E * cap, *t.shape[1:]), room, dtype=t.dtype, device="cuda")
+        out[place] = t
+        return out
+    full = lambda n, v, t=TORCH[dt]: torch.full((E * cap, n), v, dtype=t, device="cuda")
+    nan, u8 = float("nan"), torch.uint8
+    h, q, scale = bm.beam_moe_swiglu(cfg, gu, weights=w, row_of_pair=row_d, keep8=True)
+    q = q.view(u8)
+    h2, q2, scale2 = bm.beam_moe_swiglu(
+        cfg, spread(gu, nan), weights=w, row_of_pair=far, h=full(I, -3.0), keep_q=full(2 * I, 9, u8),
+        keep_scale=torch.full((E * cap, *scale.shape[1:]), 9, dtype=u8, device="cuda"))
+    assert torch.equal(h2, spread(h, -3.0)) and torch.equal(q2, spread(q, 9)) and torch.equal(scale2, spread(scale, 9))
+    src, src_scale = (q, scale) if source8 else (gu, None)
+    src2, src2_scale = (q2, scale2) if source8 else (spread(gu, nan), None)
+    dgu, again, dw = bm.beam_moe_swiglu_backward(cfg, dh, src, gu_scale=src_scale, weights=w, row_of_pair=row_d)
+    dgu2, again2, dw2 = bm.beam_moe_swiglu_backward(cfg, spread(dh, nan), src2, gu_scale=src2_scale, weights=w,
+                                                    row_of_pair=far, dgu=full(2 * I, -3.0), h=full(I, -3.0))
+    assert torch.equal(dgu2, spread(dgu, -3.0)) and torch.equal(again2, spread(again, -3.0))
+    assert torch.equal(dw2, dw) and (dw[row_d < 0] == 0).all()
+
+
 def test_swiglu_offsets_past_32_bits():
     """gu with more than 2^31 elements, rows in order: the last rows are right."""
     T, K, I = 33000, 8, 4104

@@ -81,6 +81,15 @@ def test_rows_out_of_range(call):
     assert call(cfg(hidden=1 << 20, inter=1 << 20), rows=1 << 30) == ARG
 
 
+@pytest.mark.parametrize("call", ROWS)
+def test_threads_past_32_bits(call):
+    """2^35 values in the rows that an operator goes over: 2^32 threads of 8 columns."""
+    for T, width in ((1 << 20, 1 << 15), (1 << 17, 1 << 18), (1 << 27, 129), (1 << 29, 1)):
+        assert call(cfg(hidden=width, inter=width, topk=1), T=T, rows=T // 8) == ARG
+    if "swiglu" in call.__name__:                          # rows in order, a fifth of them to spare
+        assert call(cfg(inter=1 << 15, topk=1), T=(1 << 20) * 5 // 6, rows=1 << 20) == ARG
+
+
 def test_experts_out_of_range():
     for call in (sort, route_backward):
         assert call(cfg(n_experts=0)) == ARG
@@ -145,6 +154,9 @@ def test_swiglu_workspace():
     for call in (swiglu, swiglu_backward):
         assert call(c, T=T, rows=100) == WS and call(c, T=T, rows=100, ws=P, nb=need - 1) == WS
         assert call(c, T=T, rows=100, ws=ODD, nb=need) == ARG
+    pairs = 3 * T                                          # not in a buffer of more than 5/4 the pairs
+    assert bm.beam_moe_swiglu_workspace_size(c, T, pairs * 5 // 4) >= 4 * (pairs * 5 // 4)
+    assert bm.beam_moe_swiglu_workspace_size(c, T, pairs * 5 // 4 + 1) == 0
 
 
 def test_route_backward_arguments():
