@@ -13,6 +13,7 @@ constexpr int kColTile = 128;      // hidden columns of a dx block
 constexpr int kDxStride = kColTile + 4;       // 16-byte rows, neighbours four banks apart
 constexpr int kDwTokens = 32;      // tokens of one stage of a dW block
 constexpr int kDwCols = 128;       // its hidden columns
+constexpr int kBiasCols = 16;      // columns over which the bias' gradient is spread
 constexpr int kCUs = 256;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -28,11 +29,20 @@ int token_splits(int64_t T, int64_t tiles, int blocks, int least) {
     return static_cast<int>(s < 1 ? 1 : s);
 }
 
+// The bias' gradient takes part in dW's products as columns that follow the H of x: each
+// stage of tokens adds to one of them in turn, and they are added up in FP64, so that its
+// error stays that of the dz (one column for all: 15109 tokens and 4 experts twice that).
+// Few tokens need one column.  All of them lie in one tile.
+__host__ __device__ inline int bias_columns(int64_t T) { return T <= 2 * kDwTokens ? 1 : kBiasCols; }
+__host__ __device__ inline int bias_first(int H, int columns) {
+    return H % kDwCols + columns <= kDwCols ? H : H / kDwCols * kDwCols + kDwCols;
+}
+
 }  // namespace
 
 RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K) {
     RouteBackwardPlan p;
-    const int64_t tiles = (static_cast<int64_t>(H) + kDwCols) / kDwCols;     // a column for the bias
+    const int bias = bias_columns(T), tiles = bias_first(H, bias) / kDwCols + 1;
     p.splits = T == 0 ? 0 : token_splits(T, tiles, 2, 2 * kDwTokens);
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off += align256(bytes); return o; };
@@ -40,7 +50,8 @@ RouteBackwardPlan route_backward_plan(int64_t T, int H, int E, int K) {
     p.expert = take(sizeof(int32_t) * T * K);
     p.split = take(8 * T * K);
     p.live = take(T + 8);                      // read eight at a time
-    p.part = take(p.splits > 1 ? sizeof(float) * p.splits * (static_cast<size_t>(H) + 1) * E : 0);
+    // a single range writes dW itself, and the bias' columns if they are to be added up
+    p.part = take(sizeof(float) * (p.splits > 1 ? p.splits * (static_cast<size_t>(H) + bias) : bias > 1 ? bias : 0) * E);
     p.total = off;
     return p;
 }
@@ -266,8 +277,8 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
 }
 
 // ---------------------------------------------------------------------------
-// dW[h, e] = sum_t x[t, h] dz[t, e], and the bias' gradient as column h = H with x = 1, on
-// the matrix cores with the tokens as the summed index.  An FP32 value is the sum of three
+// dW[h, e] = sum_t x[t, h] dz[t, e], and the bias' gradient as columns with x = 1
+// (bias_columns), on the matrix cores with the tokens as the summed index.  An FP32 value is the sum of three
 // BF16 values (8 bits each, cut off by rounding to nearest: the rest is exact), so dz is
 // three operands, and x is one (BF16) or three (FP32, where the six products of largest
 // order are kept: the others are under 2^-24 of the result's terms).  Sums in FP32.
@@ -279,7 +290,7 @@ __global__ __launch_bounds__(1024) void route_dx(RouteBackwardArgs a, int64_t pe
 // after the products.  One buffer: two blocks share a CU (57 KB each for 256 experts and
 // BF16), and one's products run while the other writes its stage.  A stage's values are
 // loaded into registers a stage ahead.  Token ranges (blockIdx.y) write partial sums
-// [H+1, E], a single range the gradients themselves.  Matrix-bound: 32768 tokens of 5120
+// [H + bias columns, E], a single range the gradients themselves.  Matrix-bound: 32768 tokens of 5120
 // columns in BF16 take 0.21 ms, 1.2 PFLOP/s of the three products, 8192 in FP32 0.115 ms,
 // 1.1 of the six; a large library product in BF16 reaches 1.24.  The same sums as FP32
 // additions in LDS, a lane a column, took 9.8 and 2.2 ms.
@@ -323,13 +334,7 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int per_
         u32x2 live;                            // a byte each
         u32x2 pick[L::Q];                      // a thread's picks
     } ahead[2];
-    Pair<BF16> ones;                           // 1 in the bias' column
-    if constexpr (BF16) {
-        ones.w[0] = c0 + col == a.H ? 0x3F80u : c0 + col + 1 == a.H ? 0x3F800000u : 0u;
-    } else {
-        ones.w[0] = c0 + col == a.H ? 0x3F800000u : 0u;
-        ones.w[1] = c0 + col + 1 == a.H ? 0x3F800000u : 0u;
-    }
+    const int bias = bias_columns(a.T), bias0 = bias_first(a.H, bias);
     // thread -> its picks among the stage's 32 K, and their token's place in an LDS row
     int chunk[L::Q], byte[L::Q], old[L::Q];    // old: where its picks lie in LDS
 #pragma unroll
@@ -379,7 +384,14 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int per_
         }
     };
     auto fill_x = [&](const Stage& f, int t) {
-        Pair<BF16> v[L::TPW];
+        Pair<BF16> v[L::TPW], ones;            // 1 in the stage's bias column
+        const int one = bias0 + ((t / kDwTokens) & (bias - 1)) - c0 - col;
+        if constexpr (BF16) {
+            ones.w[0] = one == 0 ? 0x3F80u : one == 1 ? 0x3F800000u : 0u;
+        } else {
+            ones.w[0] = one == 0 ? 0x3F800000u : 0u;
+            ones.w[1] = one == 1 ? 0x3F800000u : 0u;
+        }
 #pragma unroll
         for (int j = 0; j < L::TPW; ++j) {
             // a token without picks is not looked at (live holds 0 or 1 a byte)
@@ -498,10 +510,12 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int per_
 #pragma unroll
     for (int j = 0; j < L::TN; ++j) {
         const int c = c0 + wn * L::NW + j * 32 + (lane & 31);
-        if (c > a.H) continue;
+        const int b = c - bias0;               // a bias column if in [0, bias)
+        if (c >= a.H && (b < 0 || b >= bias)) continue;
         float* out;
-        if (gridDim.y > 1) out = part + (static_cast<int64_t>(blockIdx.y) * (a.H + 1) + c) * a.E;
-        else out = c < a.H ? dw + static_cast<int64_t>(c) * a.E : dbias;
+        if (gridDim.y > 1) out = part + (static_cast<int64_t>(blockIdx.y) * (a.H + bias) + (c < a.H ? c : a.H + b)) * a.E;
+        else if (c < a.H) out = dw + static_cast<int64_t>(c) * a.E;
+        else out = bias > 1 ? part + b * a.E : dbias;
         if (!out) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -520,18 +534,36 @@ __global__ __launch_bounds__(256, 2) void route_dw(RouteBackwardArgs a, int per_
     }
 }
 
-// The partial sums in token order, eight loads in flight: with one, 9021 tokens of 128 columns
-// and 3 experts took 49 us a call, not 26.
-__global__ __launch_bounds__(256) void route_dw_sum(int64_t n, int64_t slice, int splits, int64_t bias_at,
-                                                    const float* __restrict__ part, float* __restrict__ dw,
-                                                    float* __restrict__ dbias) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= n) return;
-    float v = 0.0f;
+// The partial sums in token order, eight loads in flight (with one, 9021 tokens of 128 columns
+// and 3 experts took 49 us a call, not 26): blocks of 256 values of dW, `blocks` of them,
+// then blocks of 16 experts' bias, a thread a column and expert, in FP64.
+__global__ __launch_bounds__(256) void route_dw_sum(int64_t n, int64_t slice, int splits, unsigned blocks, int E,
+                                                    int bias, int64_t bias_at, const float* __restrict__ part,
+                                                    float* __restrict__ dw, float* __restrict__ dbias) {
+    if (blockIdx.x < blocks) {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+        if (i >= n) return;
+        float v = 0.0f;
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) v += part[s * slice + i];
-    if (i < bias_at) dw[i] = v;
-    else if (dbias) dbias[i - bias_at] = v;
+        for (int s = 0; s < splits; ++s) v += part[s * slice + i];
+        dw[i] = v;
+        return;
+    }
+    static_assert(kBiasCols == 16, "256 threads are 16 columns of 16 experts");
+    __shared__ double s_sum[kBiasCols][16];
+    const int b = threadIdx.x >> 4, k = threadIdx.x & 15;
+    const int e = static_cast<int>(blockIdx.x - blocks) * 16 + k;
+    double v = 0.0;
+    if (b < bias && e < E) {
+#pragma unroll 8
+        for (int s = 0; s < splits; ++s) v += part[s * slice + bias_at + b * E + e];
+    }
+    s_sum[b][k] = v;
+    __syncthreads();
+    if (b == 0 && e < E) {
+        for (int j = 1; j < bias; ++j) v += s_sum[j][k];
+        dbias[e] = static_cast<float>(v);
+    }
 }
 
 template <bool BF16, bool ALIGNED, int KT>
@@ -551,7 +583,7 @@ static void dw_launch_picks(hipStream_t st, const RouteBackwardArgs& a, int spli
     using L = DwTile<BF16, ME, Q>;
     const int per = static_cast<int>(((a.T + splits - 1) / splits + kDwTokens - 1) / kDwTokens * kDwTokens);
     lds_opt_in(reinterpret_cast<const void*>(&route_dw<BF16, EVEN, ME, Q>), L::kLds);
-    route_dw<BF16, EVEN, ME, Q><<<dim3((a.H + kDwCols) / kDwCols, splits), L::kThreads, L::kLds, st>>>(
+    route_dw<BF16, EVEN, ME, Q><<<dim3(bias_first(a.H, bias_columns(a.T)) / kDwCols + 1, splits), L::kThreads, L::kLds, st>>>(
         a, per, x, split, alive, part, dw, dbias);
 }
 
@@ -598,11 +630,14 @@ void launch_route_backward(hipStream_t st, const RouteBackwardArgs& a, const Rou
                                 : (even ? &route_backward_typed<false, true> : &route_backward_typed<false, false>);
         run(st, a, p, x, w_router, dx_add, dx, dz, expert, reinterpret_cast<const u32x2*>(split), alive, part,
             dw_router, dlogit_bias);
-        if (p.splits == 1) return;
     }
-    const int64_t slice = (static_cast<int64_t>(a.H) + 1) * a.E;
-    route_dw_sum<<<static_cast<unsigned>((slice + 255) / 256), 256, 0, st>>>(
-        slice, slice, p.splits, static_cast<int64_t>(a.H) * a.E, part, dw_router, dlogit_bias);
+    const int bias = bias_columns(a.T);
+    const int64_t values = p.splits == 1 ? 0 : static_cast<int64_t>(a.H) * a.E;      // of dW, to add up
+    const unsigned blocks = static_cast<unsigned>((values + 255) / 256);
+    const unsigned bias_blocks = dlogit_bias && (p.splits != 1 || bias > 1) ? (a.E + 15) / 16 : 0;
+    if (blocks + bias_blocks == 0) return;
+    route_dw_sum<<<blocks + bias_blocks, 256, 0, st>>>(values, values + static_cast<int64_t>(bias) * a.E, p.splits,
+                                                       blocks, a.E, bias, values, part, dw_router, dlogit_bias);
 }
 
 }  // namespace beam

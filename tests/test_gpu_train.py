@@ -588,7 +588,7 @@ def route_ref(x, wr, z, ids, gw, add, alpha):
 ROUTE = [  # T, H, E, K, drop
     (1, 1, 1, 1, 0), (1, 130, 256, 8, 0), (16, 5120, 256, 8, 0), (7, 127, 3, 2, 0.3), (33, 128, 60, 9, 0.2),
     (65, 129, 16, 6, 0.3), (200, 300, 255, 8, 0.2), (130, 64, 256, 32, 0.1), (1500, 257, 12, 3, 0.3),
-    (900, 1024, 256, 8, 0), (64, 33000, 5, 2, 0)]
+    (900, 1024, 256, 8, 0), (64, 33000, 5, 2, 0), (1100, 112, 33, 4, 0.3), (1000, 113, 20, 2, 0)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -616,6 +616,23 @@ def test_route_backward(T, H, E, K, drop, dt):
     here = add.cuda()
     bm.beam_moe_route_backward(cfg, x.cuda(), wr.cuda(), z.cuda(), ids.cuda(), gw.cuda(), dx_add=here, dx=here)
     assert torch.equal(here, dx)
+
+
+def test_route_backward_bias_of_cancelling_tokens():
+    """dz of one, of minus one 481 tokens later, and of 2^-29 in the others (exact: equal
+    logits, scores of a half).  In one FP32 sum what comes between the two is lost, 480 of
+    the 1022 small terms; spread over columns and added up in FP64 those of the two stages of
+    32 tokens are (62), and two roundings next to one are off by 2^-24, 32 terms, each."""
+    T, H = 1024, 32888                                     # one token range, the bias in a tile of its own
+    g = torch.zeros(T, 2)
+    g[:, 0] = 8 * 2.0 ** -29
+    g[31, 0], g[512, 0] = 8.0, -8.0
+    ids = torch.tensor([[0, 1]], dtype=torch.int32).repeat(T, 1)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    _, dwr, db = bm.beam_moe_route_backward(config("bf16", H=H, E=2, K=2, alpha=1.0), x, torch.zeros(H, 2, device="cuda"),
+                                            torch.zeros(T, 2, device="cuda"), ids.cuda(), g.cuda())
+    assert (dwr == 0).all()
+    within(db, np.array([1022, -1022]) * 2.0 ** -29, (62 + 2 * 32 + 1) * 2.0 ** -29, "dlogit_bias")
 
 
 def test_route_backward_same_expert_twice_and_no_tokens():
